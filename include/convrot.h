@@ -177,6 +177,31 @@ cr_status cr_quant_act_ex(const void *x, cr_dtype x_dtype, int64_t ld_x, int swi
                           uint32_t flags, hipStream_t stream);
 
 /*
+ * RMS norm of a residual stream fused into the activation preparation: the input of a
+ * transformer layer's quantized linear (cr_gemm_s8_rowscale and the other INT8-activation
+ * GEMMs) in one pass over the stream.
+ *   h[m, k] = x[m, k] + residual[m, k], added in FP32 and rounded to x_dtype (h = x without a
+ *             residual); written to sum when that is not NULL.
+ *   y[m, k] = h[m, k] * weight[k] / sqrt(mean_k(h[m, k]^2) + eps), rotated and row-quantized.
+ * The factor of the row goes into the scale alone: the codes are those of cr_quant_act_ex on
+ * h (as FP32) with pre_scale = weight, bit for bit, and x_scale is that call's scale times
+ * the FP32 value of 1 / sqrt(mean + eps) (sum and root in FP64).  A zero row gets scale 0.
+ *   x          [M, ld_x] of x_dtype (CR_BF16, CR_FP16 or CR_FP32); ld_x >= K.
+ *   residual   [M, ld_res] of x_dtype, or NULL.
+ *   sum        [M, ld_sum] of x_dtype out, or NULL (it must be NULL without a residual).  It
+ *              may be x or residual itself, with that operand's row stride.
+ *   weight     [K] float, 4-byte aligned, or NULL for ones.
+ *   eps        finite, >= 0.
+ *   x_s8, ld_s8, x_scale, flags as in cr_quant_act; rows with K_pad > CR_TWO_PASS_K_PAD
+ *   stream twice.
+ */
+cr_status cr_quant_act_rmsnorm(const void *x, cr_dtype x_dtype, int64_t ld_x,
+                               const void *residual, int64_t ld_res, void *sum, int64_t ld_sum,
+                               const float *weight, float eps, int64_t M, int64_t K,
+                               int8_t *x_s8, int64_t ld_s8, float *x_scale,
+                               uint32_t flags, hipStream_t stream);
+
+/*
  * Unfused SwiGLU to FP32 (the ComfyUI Turing Utils README compares the fused
  * SwiGLU + rotation + A8 path against an unfused activation): out[m, k] =
  * swish(h[m, k]) * h[m, F + k] with the same element arithmetic as cr_quant_act_swiglu.

@@ -60,6 +60,8 @@ def lib() -> C.CDLL:
             "cr_prep_weight_nvfp4": (C.c_int, [vp, i64, vp, i64, vp, i64, i64, vp, i64, vp, u32, vp]),
             "cr_quant_act": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, i64, vp, u32, vp]),
             "cr_quant_act_swiglu": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, i64, vp, u32, vp]),
+            "cr_quant_act_rmsnorm": (C.c_int, [vp, C.c_int, i64, vp, i64, vp, i64, vp, C.c_float, i64, i64, vp, i64,
+                                               vp, u32, vp]),
             "cr_swiglu": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, i64, vp]),
             "cr_gemm_s8_rowscale": (C.c_int, [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, C.c_int, i64, vp]),
             "cr_gemm_s8_rowscale_bias": (C.c_int, [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, vp, C.c_int, i64,
@@ -138,6 +140,17 @@ def _rows_ld(t: torch.Tensor):
     return t.shape[0], t.stride(0)
 
 
+def _dtype_code(t: torch.Tensor) -> int:
+    """cr_dtype of a tensor (-1, which every call rejects, for types the library does not know)."""
+    return _TORCH_TO_CR.get(t.dtype, -1)
+
+
+def _check_vector(name: str, t, n: int, dtype=torch.float32):
+    """An optional contiguous vector argument of at least n elements."""
+    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() < n):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements")
+
+
 def padded_k(k: int) -> int:
     return int(lib().cr_padded_k(k))
 
@@ -175,6 +188,24 @@ def cr_quant_act_ex(x, K, swiglu, pre_scale, x_s8, x_scale, flags=0, stream=None
     _check("cr_quant_act_ex", lib().cr_quant_act_ex(
         _ptr(x), _TORCH_TO_CR[x.dtype], ld_x, int(bool(swiglu)), M, K, _ptr(pre_scale), _ptr(x_s8), ld_s8,
         _ptr(x_scale), flags, _stream(stream)))
+
+
+def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=0, stream=None):
+    M, ld_x = _rows_ld(x)
+    _, ld_s8 = _rows_ld(x_s8)
+    ld_r = ld_s = 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have the shape and dtype of x")
+        _, ld_r = _rows_ld(residual)
+    if sum is not None:
+        if sum.shape != x.shape or sum.dtype != x.dtype:
+            raise ValueError("sum must have the shape and dtype of x")
+        _, ld_s = _rows_ld(sum)
+    _check_vector("weight", weight, K)
+    _check("cr_quant_act_rmsnorm", lib().cr_quant_act_rmsnorm(
+        _ptr(x), _dtype_code(x), ld_x, _ptr(residual), ld_r, _ptr(sum), ld_s, _ptr(weight), eps, M, K,
+        _ptr(x_s8), ld_s8, _ptr(x_scale), flags, _stream(stream)))
 
 
 def cr_swiglu(h, F, out, stream=None):
@@ -397,6 +428,21 @@ def quant_act(x: torch.Tensor, K: int | None = None, swiglu: bool = False, flags
     else:
         (cr_quant_act_swiglu if swiglu else cr_quant_act)(x, K, q, s, flags)
     return q, s
+
+
+def quant_act_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                      residual: torch.Tensor | None = None, sum: torch.Tensor | None = None, flags: int = 0):
+    """(x_s8 [M, K_pad] int8, x_scale [M] fp32, h) of the RMS norm of h = x + residual, the input
+    of the INT8-activation GEMMs.  h [M, K] in x's type goes to `sum` (which may be x or
+    residual: updated in place) or to a new tensor; None without a residual."""
+    M, K = x.shape
+    q = torch.empty(M, padded_k(K), dtype=torch.int8, device=x.device)
+    s = torch.empty(M, dtype=torch.float32, device=x.device)
+    if residual is not None and sum is None:
+        n = 16 // x.element_size()
+        sum = torch.empty(M, (K + n - 1) // n * n, dtype=x.dtype, device=x.device)[:, :K]
+    cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, q, s, flags)
+    return q, s, sum
 
 
 def prep_weight_nvfp4(w_fp4: torch.Tensor, w_sf: torch.Tensor, global_scale: torch.Tensor, K: int,

@@ -404,6 +404,28 @@ cr_status cr_quant_act_swiglu(const void *h, cr_dtype h_dtype, int64_t ld_h, int
     return cr_quant_act_ex(h, h_dtype, ld_h, 1, M, F, nullptr, x_s8, ld_s8, x_scale, flags, stream);
 }
 
+cr_status cr_quant_act_rmsnorm(const void *x, cr_dtype x_dtype, int64_t ld_x, const void *residual, int64_t ld_res,
+                               void *sum, int64_t ld_sum, const float *weight, float eps, int64_t M, int64_t K,
+                               int8_t *x_s8, int64_t ld_s8, float *x_scale, uint32_t flags, hipStream_t stream)
+{
+    cr_status s = check_act(x, x_dtype, ld_x, M, K, K, x_s8, ld_s8, x_scale, flags);
+    if (s != CR_OK) return s;
+    if (!(eps >= 0.0f) || eps > 3.402823466e38f) return CR_ERR_INVALID_ARG;
+    if (sum && !residual) return CR_ERR_INVALID_ARG;
+    if ((residual && ld_res < K) || (sum && ld_sum < K)) return CR_ERR_INVALID_ARG;
+    const int64_t es = elem_size(x_dtype);
+    if (residual && (!aligned(residual, 16) || (ld_res * es) % 16 != 0)) return CR_ERR_MISALIGNED;
+    if (sum && (!aligned(sum, 16) || (ld_sum * es) % 16 != 0)) return CR_ERR_MISALIGNED;
+    if ((sum && sum == x && ld_sum != ld_x) || (sum && sum == residual && ld_sum != ld_res)) return CR_ERR_INVALID_ARG;
+    if (weight && !aligned(weight, 4)) return CR_ERR_MISALIGNED;
+    if (M == 0) return CR_OK;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    return from_hip(convrot::launch_quant_act_rmsnorm(x, (int)x_dtype, ld_x, residual, ld_res, sum, ld_sum, weight,
+                                                      eps, M, K, x_s8, ld_s8, x_scale,
+                                                      (flags & CR_FLAG_FORCE_TWO_PASS) != 0,
+                                                      (flags & CR_FLAG_BLOCK_TRANSPOSED) != 0, stream));
+}
+
 cr_status cr_swiglu(const void *h, cr_dtype h_dtype, int64_t ld_h, int64_t M, int64_t F,
                     float *out, int64_t ld_out, hipStream_t stream)
 {
