@@ -100,7 +100,9 @@ typedef enum {
 enum {
     CR_FLAG_NONE = 0,
     CR_FLAG_FORCE_TWO_PASS = 1,   /* stream rows twice whatever their length */
-    CR_FLAG_BLOCK_TRANSPOSED = 2  /* S8 codes in block-transposed column order (below) */
+    CR_FLAG_BLOCK_TRANSPOSED = 2, /* S8 codes in block-transposed column order (below) */
+    CR_FLAG_CAUSAL = 16,          /* cr_attn_kv8: a token sees the keys up to its own */
+    CR_FLAG_ROPE_INTERLEAVED = 32 /* cr_rope_append_kv8: pairs (2i, 2i + 1), not (i, i + D/2) */
 };
 
 /* Column order of the S8 outputs of the preparation calls.  Default (natural): column k
@@ -504,6 +506,96 @@ cr_status cr_gemm_nvfp4_fused(const int8_t *a_s8, int64_t lda, const float *a_sc
                               const uint8_t *w_sf, int64_t ld_sf, const float *global_scale,
                               const float *w_amax, const float *bias, int64_t M, int64_t N, int64_t K,
                               void *c, cr_dtype c_dtype, int64_t ldc, uint32_t flags, hipStream_t stream);
+
+/*
+ * The 8-bit key/value cache of the attention between two quantized linear layers: pages of
+ * CR_KV8_PAGE tokens, E4M3 codes (OCP: bias 7, largest 448, NaN 0x7F and 0xFF), one FP32 scale
+ * for each page and key/value head, for the keys and for the values; value = code * scale.
+ *   k        [n_pages, Hkv, CR_KV8_PAGE, D] bytes, 16-byte aligned.
+ *   v        [n_pages, Hkv, D, CR_KV8_PAGE] bytes, 16-byte aligned (dim-major).
+ *   k_scale, v_scale   [n_pages, Hkv] float, positive.  cr_rope_append_kv8 writes powers of
+ *            two; cr_attn_kv8 takes any positive scales.
+ *   n_pages  pages in the cache.
+ *   page_table   [B, ld_table] int32: page p of sequence b holds its tokens p * CR_KV8_PAGE ..;
+ *            ld_table is also the most pages a sequence may have (at most CR_KV8_MAX_PAGES).
+ *            An entry outside 0 .. n_pages-1 names no page: tokens for it are not stored,
+ *            and its keys are seen by nobody.  A page that is being appended to belongs to
+ *            one sequence; pages that are only read may be shared.
+ * The pointers are device pointers; the struct itself is read on the host during the call.
+ */
+#define CR_KV8_PAGE 64
+#define CR_KV8_MAX_PAGES ((int64_t)1 << 24)
+typedef struct {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t n_pages;
+    const int32_t *page_table;
+    int64_t ld_table;
+} cr_kv8_cache;
+
+/* A ragged batch, common to the two calls below: the rows of sequence b are tokens
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 of T ([B + 1] int32, from 0, non-decreasing, at most T; a
+ * sequence whose bounds are out of order or beyond T counts as empty), and kv_lens[b] ([B] int32)
+ * is the length of sequence b in the cache including those new tokens: they are its last
+ * ones.  Both are device pointers. */
+
+/*
+ * Rotary embedding over several position axes, per-head RMS norm of queries and keys, and the
+ * append of keys and values to the cache, from the rows of a QKV projection:
+ *   qkv      [T, ld_qkv] of dtype (CR_BF16 or CR_FP16): Hq query heads, Hkv key heads, Hkv
+ *            value heads of D elements (D 64 or 128); rows of 16-byte multiples.
+ *   q_out    [T, ld_q] of dtype: the normed and rotated queries.  It may be the query part of
+ *            qkv itself (q_out = qkv, ld_q = ld_qkv).  Not used when Hq = 0.
+ *   q_weight, k_weight   [D] float or NULL (no norm): x * w / sqrt(mean(x^2) + eps) per head,
+ *            before the rotation.
+ *   pos      [T, ld_pos] int32, n_axes (1..4) positions of each token.
+ *   freq, axis   [D / 2] double and [D / 2] int32: pair i turns by pos[axis[i]] * freq[i]
+ *            radians, (x, y) -> (x cos - y sin, y cos + x sin) on elements (i, i + D/2), or
+ *            (2i, 2i + 1) with CR_FLAG_ROPE_INTERLEAVED; frequency 0 leaves a pair as it is.  An
+ *            axis beyond n_axes counts as the last.  The angle is reduced in FP64.
+ *   max_new  at least the longest run of new tokens of a sequence (sizes the launch; tokens of
+ *            longer runs are not processed).
+ * Queries are rounded to dtype.  Keys (rotated, FP32) and values are coded against their page's
+ * scale: the smallest power of two >= 2^-126 with which the largest finite magnitude of the
+ * page's new tokens is at most 448, or the page's scale so far where that is larger and the
+ * page holds older tokens; where the scale grows, the older codes are divided by the growth
+ * and rounded (exact unless a code falls below 2^-6).  A value that is not finite is coded
+ * as NaN and leaves every other value alone.  Calling it again for the same tokens gives the
+ * same cache.  A sequence with kv_lens below its number of new tokens stores nothing.
+ */
+cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, int64_t T, int64_t B,
+                             const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t max_new,
+                             int64_t Hq, int64_t Hkv, int64_t D, const float *q_weight, const float *k_weight,
+                             float eps, const int32_t *pos, int64_t ld_pos, int64_t n_axes, const double *freq,
+                             const int32_t *axis, void *q_out, int64_t ld_q, const cr_kv8_cache *cache,
+                             uint32_t flags, hipStream_t stream);
+
+/*
+ * Attention over the cache, for prompts and for single tokens:
+ *   out[t, h] = sum_j p_j V[j] / sum_j p_j,  p_j = exp(sm_scale * q[t, h] . K[j]),
+ * over the keys j < kv_lens[b] of the token's sequence, and with CR_FLAG_CAUSAL only those up
+ * to the token's own position kv_lens[b] - (its run's length) + (its index in the run).  Query
+ * head h reads key/value head h / (Hq / Hkv).  A token that sees no key gives zeros.  A NaN
+ * in a key or value reaches exactly the tokens that see it.
+ *   q, out   [T, ld_q], [T, ld_out] of dtype (CR_BF16 or CR_FP16), Hq heads of D (64 or 128)
+ *            elements; rows of 16-byte multiples, 16-byte aligned.
+ *   max_q, max_kv   at least the longest run of queries, and about the longest kv_lens (they
+ *            size the launch; queries of longer runs get no output, longer caches only lose
+ *            balance).
+ *   Hq       a multiple of Hkv.      sm_scale   finite, > 0.
+ *   workspace   cr_attn_kv8_workspace_bytes(...) bytes (for the current device), 256-byte
+ *            aligned; may be NULL where that is 0.  Nothing in it needs to start at zero.
+ * Products are accumulated and softmax statistics held in FP32; probabilities are rounded to
+ * dtype for the second product.  The cache may be split into runs that are joined at the end;
+ * the result does not depend on timing.
+ */
+size_t cr_attn_kv8_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, int64_t Hkv,
+                                   int64_t D);
+cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, int64_t B,
+                      const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t max_q, int64_t max_kv,
+                      int64_t Hq, int64_t Hkv, int64_t D, const cr_kv8_cache *cache, float sm_scale,
+                      void *out, int64_t ld_out, void *workspace, size_t ws_bytes, uint32_t flags,
+                      hipStream_t stream);
 
 #ifdef __cplusplus
 }

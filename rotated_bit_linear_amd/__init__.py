@@ -22,6 +22,8 @@ from . import build as _build
 CR_ABI_VERSION = 3
 CR_BF16, CR_FP16, CR_FP32, CR_I32 = 0, 1, 2, 3
 CR_FLAG_NONE, CR_FLAG_FORCE_TWO_PASS, CR_FLAG_BLOCK_TRANSPOSED = 0, 1, 2
+CR_FLAG_CAUSAL, CR_FLAG_ROPE_INTERLEAVED = 16, 32
+KV8_PAGE = 64
 CR_MAX_K_PAD = 133120
 NOALLOC_SCRATCH_BYTES = 64 << 20
 DEFAULT_MAX_TILE_BYTES = 128 << 20
@@ -34,6 +36,12 @@ _CR_TO_TORCH = {v: k for k, v in _TORCH_TO_CR.items()}
 
 LIB_PATH = _build.LIB
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "convrot.h")
+
+
+class _Kv8(C.Structure):
+    """cr_kv8_cache"""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n_pages", C.c_int64), ("page_table", C.c_void_p), ("ld_table", C.c_int64)]
 
 
 class CrError(RuntimeError):
@@ -93,6 +101,11 @@ def lib() -> C.CDLL:
             "cr_linear_w4a4_e2m3_workspace_bytes": (sz, [i64, i64]),
             "cr_linear_w4a4_e2m3": (C.c_int, [vp, C.c_int, i64, C.c_int, i64, i64, vp, i64, vp, i64, vp, vp,
                                               C.c_int, i64, vp, sz, u32, vp]),
+            "cr_rope_append_kv8": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, vp, i64, i64, i64, i64, vp, vp, C.c_float,
+                                             vp, i64, i64, vp, vp, vp, i64, C.POINTER(_Kv8), u32, vp]),
+            "cr_attn_kv8_workspace_bytes": (sz, [i64, i64, i64, i64, i64, i64, i64]),
+            "cr_attn_kv8": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, vp, i64, i64, i64, i64, i64, C.POINTER(_Kv8),
+                                      C.c_float, vp, i64, vp, sz, u32, vp]),
             "cr_gemm_nvfp4_fused": (C.c_int, [vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp,
                                               C.c_int, i64, u32, vp]),
         }
@@ -412,6 +425,84 @@ def cr_linear_w4a4_e2m3(x, K, swiglu, w_f6, w_scale, out, workspace, bias=None, 
         0 if workspace is None else workspace.numel() * workspace.element_size(), flags, _stream(stream)))
 
 
+class Kv8Cache:
+    """The 8-bit paged key/value cache: k [pages, Hkv, 64, D] and v [pages, Hkv, D, 64] uint8 (E4M3
+    codes), k_scale and v_scale [pages, Hkv] fp32.  The caller deals out the pages: a page table
+    [B, pages per sequence] int32 goes with every call."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or v.dim() != 4 or k.shape[2] != KV8_PAGE or v.shape != (*k.shape[:2], k.shape[3], KV8_PAGE):
+            raise ValueError("expected k [pages, Hkv, 64, D] and v [pages, Hkv, D, 64]")
+        for t, dtype, shape in ((k, torch.uint8, k.shape), (v, torch.uint8, v.shape),
+                                (k_scale, torch.float32, k.shape[:2]), (v_scale, torch.float32, k.shape[:2])):
+            if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+                raise ValueError("codes must be contiguous uint8, scales contiguous fp32 [pages, Hkv]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.n_pages, self.Hkv, _, self.D = k.shape
+
+    @classmethod
+    def empty(cls, n_pages: int, Hkv: int, D: int, device="cuda") -> "Kv8Cache":
+        codes = lambda *shape: torch.empty(n_pages, Hkv, *shape, dtype=torch.uint8, device=device)  # noqa: E731
+        scales = lambda: torch.empty(n_pages, Hkv, dtype=torch.float32, device=device)  # noqa: E731
+        return cls(codes(KV8_PAGE, D), codes(D, KV8_PAGE), scales(), scales())
+
+    def _with_table(self, page_table: torch.Tensor) -> _Kv8:
+        return _Kv8(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                    self.n_pages, page_table.data_ptr(), page_table.shape[1])
+
+
+def _check_batch(cu_seqlens, kv_lens, page_table):
+    B = kv_lens.shape[0]
+    if cu_seqlens.dtype != torch.int32 or kv_lens.dtype != torch.int32 or cu_seqlens.numel() != B + 1 \
+            or not cu_seqlens.is_contiguous() or not kv_lens.is_contiguous():
+        raise ValueError("cu_seqlens [B + 1] and kv_lens [B] must be contiguous int32 tensors")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 tensor [B, pages per sequence]")
+    return B
+
+
+def cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight, eps, pos, freq, axis, q_out, cache,
+                       page_table, flags=0, stream=None):
+    T, ld = _rows_ld(qkv)
+    B = _check_batch(cu_seqlens, kv_lens, page_table)
+    D, Hkv = cache.D, cache.Hkv
+    if qkv.shape[1] != (Hq + 2 * Hkv) * D:
+        raise ValueError(f"qkv must hold {Hq} + 2 * {Hkv} heads of {D} elements a row")
+    _, ld_q = _rows_ld(q_out)
+    if q_out.dtype != qkv.dtype or q_out.shape != (T, Hq * D):
+        raise ValueError("q_out must be [T, Hq * D] of qkv's dtype")
+    n_pos, ld_pos = _rows_ld(pos)
+    if pos.dtype != torch.int32 or n_pos != T:
+        raise ValueError("pos must be int32 [T, axes]")
+    for name, t, dtype in (("q_weight", q_weight, torch.float32), ("k_weight", k_weight, torch.float32)):
+        _check_vector(name, t, D, dtype)
+    _check_vector("freq", freq, D // 2, torch.float64)
+    _check_vector("axis", axis, D // 2, torch.int32)
+    _check("cr_rope_append_kv8", lib().cr_rope_append_kv8(
+        _ptr(qkv), _dtype_code(qkv), ld, T, B, _ptr(cu_seqlens), _ptr(kv_lens), max_new, Hq, Hkv, D, _ptr(q_weight),
+        _ptr(k_weight), eps, _ptr(pos), max(ld_pos, pos.shape[1]), pos.shape[1], _ptr(freq), _ptr(axis), _ptr(q_out),
+        max(ld_q, Hq * D), C.byref(cache._with_table(page_table)), flags, _stream(stream)))
+
+
+def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
+    return int(lib().cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D))
+
+
+def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm_scale, out, workspace, flags=0,
+                stream=None):
+    T, ld_q = _rows_ld(q)
+    B = _check_batch(cu_seqlens, kv_lens, page_table)
+    _, ld_out = _rows_ld(out)
+    if q.shape[1] != Hq * cache.D or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must be [T, Hq * D] of one dtype")
+    _check("cr_attn_kv8", lib().cr_attn_kv8(
+        _ptr(q), _dtype_code(q), max(ld_q, q.shape[1]), T, B, _ptr(cu_seqlens), _ptr(kv_lens), max_q, max_kv, Hq,
+        cache.Hkv, cache.D, C.byref(cache._with_table(page_table)), sm_scale, _ptr(out), max(ld_out, q.shape[1]),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), flags,
+        _stream(stream)))
+
+
 # ---------------------------------------------------------------- conveniences ----
 
 def quant_act(x: torch.Tensor, K: int | None = None, swiglu: bool = False, flags: int = 0,
@@ -576,4 +667,43 @@ def repack_w4_e2m3(w_s4: torch.Tensor, K_pad: int | None = None):
     kp = 2 * w_s4.shape[1] if K_pad is None else K_pad
     out = torch.zeros((w_s4.shape[0] + 3) // 4, 3 * kp, dtype=torch.uint8, device=w_s4.device)
     cr_repack_w4_e2m3(w_s4, out, K_pad=kp)
+    return out
+
+
+def rope_table(D: int, sections=None, base: float = 10000.0, device="cuda"):
+    """(freq [D/2] fp64, axis [D/2] int32) of a rotary embedding whose pairs are dealt to the
+    position axes in runs of `sections` (default: one axis); pair i of an axis with n pairs turns
+    by base^(-i/n) radians a position.  Pairs past the sections are left alone (frequency 0)."""
+    sections = [D // 2] if sections is None else list(sections)
+    if sum(sections) > D // 2 or not 1 <= len(sections) <= 4:
+        raise ValueError("one to four sections of at most D/2 pairs in all")
+    freq = [base ** (-i / n) for n in sections for i in range(n)]
+    axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    rest = D // 2 - len(freq)
+    return (torch.tensor(freq + [0.0] * rest, dtype=torch.float64, device=device),
+            torch.tensor(axis + [0] * rest, dtype=torch.int32, device=device))
+
+
+def rope_append_kv8(qkv, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_new: int, Hq: int, pos, freq, axis,
+                    q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False, out=None):
+    """The rotated (and, with weights, per-head normed) queries [T, Hq * D] of the rows of a QKV
+    projection; their keys and values go to the cache.  kv_lens counts the new tokens.  `out` may
+    be qkv[:, : Hq * D]."""
+    if out is None:
+        out = torch.empty(qkv.shape[0], Hq * cache.D, dtype=qkv.dtype, device=qkv.device)
+    cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight, eps, pos, freq, axis, out, cache,
+                       page_table, CR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
+    return out
+
+
+def attn_kv8(q, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_q: int, max_kv: int, Hq: int,
+             sm_scale: float | None = None, causal: bool = True, out=None, workspace=None):
+    """Attention of q [T, Hq * D] over the cached keys and values; sm_scale defaults to 1/sqrt(D)."""
+    if out is None:
+        out = torch.empty(q.shape[0], Hq * cache.D, dtype=q.dtype, device=q.device)
+    if workspace is None:
+        need = cr_attn_kv8_workspace_bytes(q.shape[0], kv_lens.shape[0], max_q, max_kv, Hq, cache.Hkv, cache.D)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table,
+                cache.D ** -0.5 if sm_scale is None else sm_scale, out, workspace, CR_FLAG_CAUSAL if causal else 0)
     return out

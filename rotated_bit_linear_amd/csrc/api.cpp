@@ -340,6 +340,60 @@ size_t noalloc_tile_bound(int64_t M, int64_t K)
     return rows < T ? 0 : (size_t)rows * (size_t)kp;
 }
 
+// ---- the 8-bit cache ----
+
+constexpr int64_t kMaxHeads = 65535;
+
+// what the two calls over the cache have in common; `needs_cache` false: no head reads or
+// writes it.  Pointers are only needed when there are tokens.
+cr_status check_kv8(cr_dtype dt, int64_t T, int64_t B, const int32_t *cu, const int32_t *kv_lens, int64_t Hq,
+                    int64_t Hkv, int64_t D, const cr_kv8_cache *c, bool needs_cache)
+{
+    if (dt != CR_BF16 && dt != CR_FP16) return CR_ERR_UNSUPPORTED_DTYPE;
+    if (T < 0 || B < 0 || T > kMaxRows || B > kMaxRows) return CR_ERR_INVALID_ARG;
+    if (Hq < 0 || Hkv < 0 || Hq > kMaxHeads || Hkv > kMaxHeads || (D != 64 && D != 128)) return CR_ERR_INVALID_ARG;
+    const bool any = T > 0 && B > 0;
+    if (any && (!cu || !kv_lens)) return CR_ERR_INVALID_ARG;
+    if (!aligned(cu, 4) || !aligned(kv_lens, 4)) return CR_ERR_MISALIGNED;
+    if (!needs_cache) return CR_OK;
+    if (!c) return CR_ERR_INVALID_ARG;
+    if (c->n_pages < 0 || c->ld_table < 0) return CR_ERR_INVALID_ARG;
+    if (c->ld_table > CR_KV8_MAX_PAGES || c->n_pages > kMaxRows) return CR_ERR_TOO_LARGE;
+    if (any && (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table)) return CR_ERR_INVALID_ARG;
+    if (any && (c->n_pages < 1 || c->ld_table < 1)) return CR_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+        !aligned(c->page_table, 4))
+        return CR_ERR_MISALIGNED;
+    return CR_OK;
+}
+
+// rows [T, ld] of 16-bit elements holding `cols` of them
+cr_status check_rows16(const void *p, int64_t ld, int64_t cols, bool any)
+{
+    if (any && !p) return CR_ERR_INVALID_ARG;
+    if (ld < cols) return CR_ERR_INVALID_ARG;
+    return (!aligned(p, 16) || ld % 8 != 0) ? CR_ERR_MISALIGNED : CR_OK;
+}
+
+convrot::Kv8Ptrs kv8_ptrs(const cr_kv8_cache *c)
+{
+    if (!c) return convrot::Kv8Ptrs{};
+    return convrot::Kv8Ptrs{c->k, c->v, c->k_scale, c->v_scale, c->n_pages, c->page_table, c->ld_table};
+}
+
+// the attention's plan on the current device; false where its sizes are not a valid call's or
+// exceed what the launch can count
+bool attn_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, int64_t Hkv, int64_t D,
+               convrot::AttnPlan *p)
+{
+    if (T < 0 || B < 0 || max_q < 0 || max_kv < 0 || T > kMaxRows || B > kMaxRows || max_q > kMaxRows) return false;
+    if (Hq < 1 || Hkv < 1 || Hq > kMaxHeads || Hq % Hkv != 0 || (D != 64 && D != 128)) return false;
+    if (max_q > T) max_q = T;
+    if (max_kv > CR_KV8_MAX_PAGES * CR_KV8_PAGE) max_kv = CR_KV8_MAX_PAGES * CR_KV8_PAGE;
+    *p = convrot::plan_attn_kv8(T, B, max_q, max_kv, (int)Hq, (int)Hkv, (int)D, current_cus());
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -970,6 +1024,82 @@ cr_status cr_linear_nvfp4_noalloc(const void *x, cr_dtype x_dtype, int64_t ld_x,
     return cr_linear_nvfp4_ex(x, x_dtype, ld_x, swiglu, M, K, pre_scale, w_fp4, ld_fp4, w_sf, ld_sf, global_scale,
                               N, bias, out, out_dtype, ldc, ws, CR_NOALLOC_SCRATCH_BYTES, bound, flags, stream,
                               nullptr);
+}
+
+cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, int64_t T, int64_t B,
+                             const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t max_new,
+                             int64_t Hq, int64_t Hkv, int64_t D, const float *q_weight, const float *k_weight,
+                             float eps, const int32_t *pos, int64_t ld_pos, int64_t n_axes, const double *freq,
+                             const int32_t *axis, void *q_out, int64_t ld_q, const cr_kv8_cache *cache,
+                             uint32_t flags, hipStream_t stream)
+{
+    cr_status s = check_kv8(dtype, T, B, cu_seqlens, kv_lens, Hq, Hkv, D, cache, Hkv > 0);
+    if (s != CR_OK) return s;
+    const bool any = T > 0 && B > 0 && Hq + Hkv > 0;
+    if (flags & ~(uint32_t)CR_FLAG_ROPE_INTERLEAVED) return CR_ERR_INVALID_ARG;
+    if (max_new < 0 || n_axes < 1 || n_axes > 4 || ld_pos < n_axes) return CR_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || eps > 3.402823466e38f) return CR_ERR_INVALID_ARG;
+    if ((s = check_rows16(qkv, ld_qkv, (Hq + 2 * Hkv) * D, any)) != CR_OK) return s;
+    if (Hq > 0 && (s = check_rows16(q_out, ld_q, Hq * D, any)) != CR_OK) return s;
+    if (q_out && q_out == qkv && Hq > 0 && ld_q != ld_qkv) return CR_ERR_INVALID_ARG;
+    if (any && (!pos || !freq || !axis)) return CR_ERR_INVALID_ARG;
+    if (!aligned(pos, 4) || !aligned(freq, 8) || !aligned(axis, 4) || !aligned(q_weight, 4) || !aligned(k_weight, 4))
+        return CR_ERR_MISALIGNED;
+    if (max_new > T) max_new = T;
+    if (!any || max_new == 0) return CR_OK;
+    // workgroups of 256 threads, at most one per page visited and head; a dispatch counts work-items in 32 bits
+    const int64_t visits = (max_new + CR_KV8_PAGE - 2) / CR_KV8_PAGE + 1;
+    if (B > (int64_t)(UINT32_MAX / 256) / visits / (Hq + Hkv)) return CR_ERR_TOO_LARGE;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    convrot::RopeLaunch r{};
+    r.qkv = qkv; r.dtype = (int)dtype; r.ld_qkv = ld_qkv; r.q_out = q_out; r.ld_q = ld_q;
+    r.q_weight = q_weight; r.k_weight = k_weight; r.eps = eps;
+    r.pos = pos; r.ld_pos = ld_pos; r.n_axes = (int)n_axes; r.freq = freq; r.axis = axis;
+    r.interleaved = (flags & CR_FLAG_ROPE_INTERLEAVED) != 0;
+    r.T = T; r.B = B; r.max_new = max_new; r.cu = cu_seqlens; r.kv_lens = kv_lens;
+    r.Hq = (int)Hq; r.Hkv = (int)Hkv; r.D = (int)D; r.cache = kv8_ptrs(Hkv > 0 ? cache : nullptr);
+    r.cus = current_cus();
+    return from_hip(convrot::launch_rope_append_kv8(r, stream));
+}
+
+size_t cr_attn_kv8_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, int64_t Hkv,
+                                   int64_t D)
+{
+    convrot::AttnPlan p;
+    return attn_plan(T, B, max_q, max_kv, Hq, Hkv, D, &p) ? p.bytes : 0;
+}
+
+cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, int64_t B,
+                      const int32_t *cu_seqlens, const int32_t *kv_lens, int64_t max_q, int64_t max_kv,
+                      int64_t Hq, int64_t Hkv, int64_t D, const cr_kv8_cache *cache, float sm_scale,
+                      void *out, int64_t ld_out, void *workspace, size_t ws_bytes, uint32_t flags,
+                      hipStream_t stream)
+{
+    cr_status s = check_kv8(dtype, T, B, cu_seqlens, kv_lens, Hq, Hkv, D, cache, true);
+    if (s != CR_OK) return s;
+    const bool any = T > 0 && B > 0;
+    if (flags & ~(uint32_t)CR_FLAG_CAUSAL) return CR_ERR_INVALID_ARG;
+    if (!(sm_scale > 0.0f) || sm_scale > 3.402823466e38f) return CR_ERR_INVALID_ARG;
+    convrot::AttnPlan p;
+    if (!attn_plan(T, B, max_q, max_kv, Hq, Hkv, D, &p)) return CR_ERR_INVALID_ARG;
+    if ((s = check_rows16(q, ld_q, Hq * D, any)) != CR_OK) return s;
+    if ((s = check_rows16(out, ld_out, Hq * D, any)) != CR_OK) return s;
+    if (any && p.bytes > 0) {
+        if (!workspace) return CR_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return CR_ERR_MISALIGNED;
+        if (ws_bytes < p.bytes) return CR_ERR_TOO_LARGE;
+    }
+    if (!any || max_q == 0) return CR_OK;
+    // workgroups of 256 threads; a dispatch counts work-items in 32 bits
+    const int64_t most = (int64_t)(UINT32_MAX / 256);
+    if (B > most / Hkv / p.row_blocks / p.splits || T > 4 * most / Hq) return CR_ERR_TOO_LARGE;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    convrot::AttnLaunch l{};
+    l.q = q; l.dtype = (int)dtype; l.ld_q = ld_q; l.out = out; l.ld_out = ld_out; l.T = T; l.B = B;
+    l.cu = cu_seqlens; l.kv_lens = kv_lens; l.Hq = (int)Hq; l.Hkv = (int)Hkv; l.D = (int)D;
+    l.cache = kv8_ptrs(cache); l.sm_scale = sm_scale; l.causal = (flags & CR_FLAG_CAUSAL) != 0;
+    l.workspace = workspace; l.plan = p;
+    return from_hip(convrot::launch_attn_kv8(l, stream));
 }
 
 }  // extern "C"

@@ -86,5 +86,63 @@ hipError_t launch_gemm_nvfp4_fused(const int8_t *A, int64_t lda, const float *sa
                                    const float *amax, const float *bias, int64_t M, int64_t N, int64_t K,
                                    void *C, int out_dtype, int64_t ldc, bool transposed, hipStream_t st);
 
+// the 8-bit cache (kv8.hpp) and its page table
+struct Kv8Ptrs {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t n_pages;
+    const int32_t *table;
+    int64_t ld_table;
+};
+
+// rotary embedding, per-head norm and append to the cache (dtype 0 bf16, 1 fp16; D 64 or 128)
+struct RopeLaunch {
+    const void *qkv;
+    int dtype;
+    int64_t ld_qkv;
+    void *q_out;
+    int64_t ld_q;
+    const float *q_weight, *k_weight;
+    float eps;
+    const int32_t *pos;
+    int64_t ld_pos;
+    int n_axes;
+    const double *freq;
+    const int32_t *axis;
+    int interleaved;
+    int64_t T, B, max_new;
+    const int32_t *cu, *kv_lens;
+    int Hq, Hkv, D;
+    Kv8Ptrs cache;
+    int cus;
+};
+hipError_t launch_rope_append_kv8(const RopeLaunch &r, hipStream_t st);
+
+// attention over the cache: which kernel runs and how the cache is split (attn_kv8.hip)
+struct AttnPlan {
+    bool few;                // few query rows a kv head: one wave holds them all
+    int64_t row_blocks;      // blocks of query rows a sequence and kv head
+    int64_t pages_per_split;
+    int64_t splits;          // 1: the kernel writes the output itself
+    size_t off_ml, bytes;    // workspace: partial outputs, then (maximum, sum) pairs
+};
+AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int Hq, int Hkv, int D, int cus);
+
+struct AttnLaunch {
+    const void *q;
+    int dtype;
+    int64_t ld_q;
+    void *out;
+    int64_t ld_out;
+    int64_t T, B;
+    const int32_t *cu, *kv_lens;
+    int Hq, Hkv, D;
+    Kv8Ptrs cache;
+    float sm_scale;
+    int causal;
+    void *workspace;
+    AttnPlan plan;
+};
+hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st);
 
 }  // namespace convrot
