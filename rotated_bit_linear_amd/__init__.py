@@ -136,8 +136,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:                             # the current stream's handle, without a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -149,8 +149,9 @@ def _check(fn: str, status: int):
 
 
 def _rows_ld(t: torch.Tensor):
-    assert t.dim() == 2 and t.stride(1) == 1, "expected a row-major 2-D tensor (unit column stride)"
-    return t.shape[0], t.stride(0)
+    st = t.stride()
+    assert len(st) == 2 and st[1] == 1, "expected a row-major 2-D tensor (unit column stride)"
+    return t.size(0), st[0]
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -205,20 +206,21 @@ def cr_quant_act_ex(x, K, swiglu, pre_scale, x_s8, x_scale, flags=0, stream=None
 
 def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=0, stream=None):
     M, ld_x = _rows_ld(x)
-    _, ld_s8 = _rows_ld(x_s8)
-    ld_r = ld_s = 0
+    r = h = None
+    ld_r = ld_h = 0
     if residual is not None:
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError("residual must have the shape and dtype of x")
-        _, ld_r = _rows_ld(residual)
+        r, ld_r = residual.data_ptr(), _rows_ld(residual)[1]
     if sum is not None:
         if sum.shape != x.shape or sum.dtype != x.dtype:
             raise ValueError("sum must have the shape and dtype of x")
-        _, ld_s = _rows_ld(sum)
+        h, ld_h = sum.data_ptr(), _rows_ld(sum)[1]
     _check_vector("weight", weight, K)
-    _check("cr_quant_act_rmsnorm", lib().cr_quant_act_rmsnorm(
-        _ptr(x), _dtype_code(x), ld_x, _ptr(residual), ld_r, _ptr(sum), ld_s, _ptr(weight), eps, M, K,
-        _ptr(x_s8), ld_s8, _ptr(x_scale), flags, _stream(stream)))
+    status = lib().cr_quant_act_rmsnorm(
+        x.data_ptr(), _dtype_code(x), ld_x, r, ld_r, h, ld_h, _ptr(weight), eps, M, K, x_s8.data_ptr(),
+        _rows_ld(x_s8)[1], x_scale.data_ptr(), flags, _stream(stream))
+    _check("cr_quant_act_rmsnorm", status)
 
 
 def cr_swiglu(h, F, out, stream=None):
@@ -448,15 +450,15 @@ class Kv8Cache:
 
     def _with_table(self, page_table: torch.Tensor) -> _Kv8:
         return _Kv8(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                    self.n_pages, page_table.data_ptr(), page_table.shape[1])
+                    self.n_pages, page_table.data_ptr(), page_table.size(1))
 
 
 def _check_batch(cu_seqlens, kv_lens, page_table):
-    B = kv_lens.shape[0]
+    B = kv_lens.numel()
     if cu_seqlens.dtype != torch.int32 or kv_lens.dtype != torch.int32 or cu_seqlens.numel() != B + 1 \
             or not cu_seqlens.is_contiguous() or not kv_lens.is_contiguous():
         raise ValueError("cu_seqlens [B + 1] and kv_lens [B] must be contiguous int32 tensors")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.size(0) != B \
             or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 tensor [B, pages per sequence]")
     return B
@@ -467,22 +469,24 @@ def cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight
     T, ld = _rows_ld(qkv)
     B = _check_batch(cu_seqlens, kv_lens, page_table)
     D, Hkv = cache.D, cache.Hkv
-    if qkv.shape[1] != (Hq + 2 * Hkv) * D:
+    if qkv.size(1) != (Hq + 2 * Hkv) * D:
         raise ValueError(f"qkv must hold {Hq} + 2 * {Hkv} heads of {D} elements a row")
-    _, ld_q = _rows_ld(q_out)
     if q_out.dtype != qkv.dtype or q_out.shape != (T, Hq * D):
         raise ValueError("q_out must be [T, Hq * D] of qkv's dtype")
+    n_axes = pos.size(-1)
     n_pos, ld_pos = _rows_ld(pos)
     if pos.dtype != torch.int32 or n_pos != T:
         raise ValueError("pos must be int32 [T, axes]")
-    for name, t, dtype in (("q_weight", q_weight, torch.float32), ("k_weight", k_weight, torch.float32)):
-        _check_vector(name, t, D, dtype)
+    _check_vector("q_weight", q_weight, D)
+    _check_vector("k_weight", k_weight, D)
     _check_vector("freq", freq, D // 2, torch.float64)
     _check_vector("axis", axis, D // 2, torch.int32)
-    _check("cr_rope_append_kv8", lib().cr_rope_append_kv8(
-        _ptr(qkv), _dtype_code(qkv), ld, T, B, _ptr(cu_seqlens), _ptr(kv_lens), max_new, Hq, Hkv, D, _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(pos), max(ld_pos, pos.shape[1]), pos.shape[1], _ptr(freq), _ptr(axis), _ptr(q_out),
-        max(ld_q, Hq * D), C.byref(cache._with_table(page_table)), flags, _stream(stream)))
+    status = lib().cr_rope_append_kv8(
+        qkv.data_ptr(), _dtype_code(qkv), ld, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_new, Hq, Hkv, D,
+        _ptr(q_weight), _ptr(k_weight), eps, pos.data_ptr(), max(ld_pos, n_axes), n_axes, freq.data_ptr(),
+        axis.data_ptr(), q_out.data_ptr(), max(_rows_ld(q_out)[1], Hq * D), cache._with_table(page_table), flags,
+        _stream(stream))
+    _check("cr_rope_append_kv8", status)
 
 
 def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
@@ -493,14 +497,14 @@ def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm
                 stream=None):
     T, ld_q = _rows_ld(q)
     B = _check_batch(cu_seqlens, kv_lens, page_table)
-    _, ld_out = _rows_ld(out)
-    if q.shape[1] != Hq * cache.D or out.shape != q.shape or out.dtype != q.dtype:
+    D, width = cache.D, Hq * cache.D
+    if q.size(1) != width or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("q and out must be [T, Hq * D] of one dtype")
-    _check("cr_attn_kv8", lib().cr_attn_kv8(
-        _ptr(q), _dtype_code(q), max(ld_q, q.shape[1]), T, B, _ptr(cu_seqlens), _ptr(kv_lens), max_q, max_kv, Hq,
-        cache.Hkv, cache.D, C.byref(cache._with_table(page_table)), sm_scale, _ptr(out), max(ld_out, q.shape[1]),
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), flags,
-        _stream(stream)))
+    status = lib().cr_attn_kv8(
+        q.data_ptr(), _dtype_code(q), max(ld_q, width), T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_q, max_kv,
+        Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), max(_rows_ld(out)[1], width),
+        _ptr(workspace), 0 if workspace is None else workspace.nbytes, flags, _stream(stream))
+    _check("cr_attn_kv8", status)
 
 
 # ---------------------------------------------------------------- conveniences ----
@@ -527,11 +531,12 @@ def quant_act_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: 
     of the INT8-activation GEMMs.  h [M, K] in x's type goes to `sum` (which may be x or
     residual: updated in place) or to a new tensor; None without a residual."""
     M, K = x.shape
-    q = torch.empty(M, padded_k(K), dtype=torch.int8, device=x.device)
-    s = torch.empty(M, dtype=torch.float32, device=x.device)
+    d = x.device
+    q = torch.empty((M, (K + 255) // 256 * 256), dtype=torch.int8, device=d)
+    s = torch.empty(M, dtype=torch.float32, device=d)
     if residual is not None and sum is None:
         n = 16 // x.element_size()
-        sum = torch.empty(M, (K + n - 1) // n * n, dtype=x.dtype, device=x.device)[:, :K]
+        sum = x.new_empty(M, K) if K % n == 0 else x.new_empty(M, (K + n - 1) // n * n)[:, :K]
     cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, q, s, flags)
     return q, s, sum
 
@@ -690,7 +695,7 @@ def rope_append_kv8(qkv, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_n
     projection; their keys and values go to the cache.  kv_lens counts the new tokens.  `out` may
     be qkv[:, : Hq * D]."""
     if out is None:
-        out = torch.empty(qkv.shape[0], Hq * cache.D, dtype=qkv.dtype, device=qkv.device)
+        out = qkv.new_empty(qkv.size(0), Hq * cache.D)
     cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight, eps, pos, freq, axis, out, cache,
                        page_table, CR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
     return out
@@ -700,9 +705,9 @@ def attn_kv8(q, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_q: int, ma
              sm_scale: float | None = None, causal: bool = True, out=None, workspace=None):
     """Attention of q [T, Hq * D] over the cached keys and values; sm_scale defaults to 1/sqrt(D)."""
     if out is None:
-        out = torch.empty(q.shape[0], Hq * cache.D, dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.size(0), Hq * cache.D)
     if workspace is None:
-        need = cr_attn_kv8_workspace_bytes(q.shape[0], kv_lens.shape[0], max_q, max_kv, Hq, cache.Hkv, cache.D)
+        need = cr_attn_kv8_workspace_bytes(q.size(0), kv_lens.numel(), max_q, max_kv, Hq, cache.Hkv, cache.D)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table,
                 cache.D ** -0.5 if sm_scale is None else sm_scale, out, workspace, CR_FLAG_CAUSAL if causal else 0)

@@ -11,8 +11,9 @@
 // the contraction may take keys in any order, so V^T is presented in the order in which S^T
 // leaves them.
 // Precision: codes are exact in bf16 and fp16, products accumulate in FP32, maximum and sum
-// are FP32.  P is rounded to the type of the queries (half a step, 2^-9 or 2^-12 of each
-// p; errors of different keys are independent), as is the output.
+// are FP32.  P is rounded to fp16 whatever the queries' type (half a step is 2^-12 of p, and
+// 2^-25 below 2^-14; the second product takes the codes as fp16): in bf16 its rounding
+// would double the variance of a bf16 output's error.
 // Scales: a page's key scale joins the factor of the exponent's argument, its value scale
 // the exponent: P holds p * vs / vref, vref the largest value scale so far (the accumulators
 // are rescaled when it grows), so 16-bit P never overflows.  A value scale below 2^-64 vref
@@ -26,6 +27,8 @@
 // put into the scores of the rows that do see it.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "kernels.hpp"
 #include "kv8.hpp"
@@ -122,49 +125,92 @@ __device__ __forceinline__ uint32_t below_bytes(int left)
     return left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
 }
 
+// the larger of the two lanes l and l ^ 32, in both
+__device__ __forceinline__ float both_halves_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// a value the compiler cannot derive from earlier ones: what follows from it is computed where
+// it is needed instead of staying in registers over the main loop
+__device__ __forceinline__ int opaque_lane(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// pins the computation of v to this place (the compiler would sink it out of the products' shadow)
+__device__ __forceinline__ void stay(float &v) { asm volatile("" : "+v"(v)); }
+
+// a barrier that waits for this wave's LDS operations but the last `younger` (its operand reads)
+template <int younger>
+__device__ __forceinline__ void barrier_but()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(younger) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// 16 codes at a uniform address, kept in scalar registers, and a lane's 32-bit offset
+typedef const __attribute__((address_space(1))) uint8_t *global_u8;
+typedef const __attribute__((address_space(1))) u32x4v *global_u32x4;
+__device__ __forceinline__ u32x4v load_codes(const uint8_t *base, uint32_t off)
+{
+    global_u8 p = (global_u8)base;
+    asm volatile("" : "+s"(p));
+    return *(global_u32x4)(p + off);
+}
+
 constexpr float kLow = -1e30f;    // running maximum before the first key
 constexpr float kSlack = 8.0f;    // log2: how far scores may exceed the running maximum
 
 // the factor of a page's scores and the shift of its exponents
 __device__ __forceinline__ float score_factor(float factor, float ks) { return fmaxf(factor * ks, 1e-37f); }
 
-// per-sequence facts of a workgroup
+// per-sequence facts of a workgroup (the launch's limits keep n * G and the keys within an int)
 struct Seq {
-    int64_t t0, n, kv, rows;
+    int64_t t0;
+    int n, kv, rows;
 };
 __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b)
 {
     Seq s;
-    batch_rows(a.batch, b, s.t0, s.n);
-    s.kv = batch_kv(a.batch, b);
+    int64_t n;
+    batch_rows(a.batch, b, s.t0, n);
+    s.n = (int)n;
+    s.kv = (int)batch_kv(a.batch, b);
     s.rows = s.n * a.G;
     return s;
 }
 // number of keys that token i of the sequence sees
-__device__ __forceinline__ int64_t visible(const AttnArgs &a, const Seq &s, int64_t i)
+__device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 {
-    if (!a.causal) return s.kv;
-    const int64_t l = s.kv - s.n + i + 1;
-    return l < 0 ? 0 : l;
+    return a.causal ? max(s.kv - s.n + i + 1, 0) : s.kv;
 }
 
 }  // namespace
 
 // ------------------------------------------------------------------ prompts: many rows ----
-// One workgroup: 32 query rows in each of 4 waves over a run of pages.  A page is read once
-// into registers (while the page before it is multiplied), widened to 16 bits, and written to
-// one of two LDS tiles in the order in which the matrix operands want it; chunks of 16 bytes
-// are swizzled by row so that the 16 lanes of a read cover all banks.
-constexpr int kRowsWave = 32, kWaves = 4, kRowsBlock = kRowsWave * kWaves;
+// One workgroup: NC blocks of 32 query rows in each of 4 waves over a run of pages.  A page is
+// read once into registers, widened to 16 bits, and written to one of two LDS tiles in the
+// order in which the matrix operands want it; rows are padded by 16 bytes so that the 16
+// lanes of a read cover all banks.
+// Software pipeline over halves of a page (32 keys): a step issues the score products of the
+// next half, the softmax of this one under them, this half's second products, and under
+// those the widening of half a page to come; one barrier a step.
+constexpr int kWaves = 4;
 
-template <int DT, int D>
-__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a)
+template <int DT, int D, int NC>
+__global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArgs a)
 {
-    constexpr int TILE = kPage * D * 2;                 // bytes of a widened tile
+    constexpr int KROW = 2 * D + 16, VROW = 2 * kPage + 16;   // bytes of a widened row of keys, of values
     constexpr int KQ = D / 64, VQ = D / 64;             // 16-byte code loads a thread and tile
-    constexpr int KC = D / 8;                           // 16-byte chunks of a widened key row
-    __shared__ __attribute__((aligned(1024))) uint8_t ldsK[2][TILE];
-    __shared__ __attribute__((aligned(1024))) uint8_t ldsV[2][TILE];
+    constexpr int ROWS = 32 * NC * kWaves;
+    __shared__ __attribute__((aligned(16))) uint8_t ldsK[2][kPage * KROW];
+    __shared__ __attribute__((aligned(16))) uint8_t ldsV[2][D * VROW];
     __shared__ uint32_t nan_keys[3][2];                 // keys of a tile whose values hold NaN codes
 
     // longest rows first (causal), key/value heads apart by the XCDs' stride
@@ -173,209 +219,341 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a)
     const int split = rest % a.splits, block = a.row_blocks - 1 - rest / a.splits;
     const int b = unit / a.Hkv, hk = unit % a.Hkv;
     const Seq s = load_seq(a, b);
-    const int64_t r0 = (int64_t)block * kRowsBlock;
+    const int r0 = block * ROWS;
     if (r0 >= s.rows) return;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int64_t r = r0 + wave * kRowsWave + col;
-    const bool valid = r < s.rows;
-    const int64_t i_tok = valid ? r / a.G : 0;
-    const int head = hk * a.G + (valid ? (int)(r - i_tok * a.G) : 0);
-    const int64_t row = s.t0 + i_tok;
 
-    // keys seen: by this row, by the block's last row (the loop's end) and by all of its rows
-    const int64_t last = (r0 + kRowsBlock < s.rows ? r0 + kRowsBlock : s.rows) - 1;
-    const int lim = valid ? (int)visible(a, s, i_tok) : 0;
-    const int lim_all = (int)visible(a, s, r0 / a.G);
-    const int pages = ((int)visible(a, s, last / a.G) + kPage - 1) / kPage;
+    // keys seen by this lane's rows, by the block's last row (the loop's end) and by all of its rows
+    const int last = min(r0 + ROWS, s.rows) - 1;
+    const int lim_all = visible(a, s, r0 / a.G);
+    const int pages = (visible(a, s, last / a.G) + kPage - 1) / kPage;
     const int p0 = (int)(split * a.pages_per_split);
     const int p1 = split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
     if (a.splits > 1 && p0 >= p1) return;               // no row of the block looks here
 
-    u32x4v q[D / 16];
+    int lim[NC];
+    u32x4v q[NC][D / 16];
 #pragma unroll
-    for (int k = 0; k < D / 16; k++)
-        q[k] = valid ? *reinterpret_cast<const u32x4v *>(a.q + row * a.ld_q + (int64_t)head * D + 16 * k + 8 * half)
-                     : u32x4v{0u, 0u, 0u, 0u};
-
-    // ---- staging ----
-    u32x4v kreg[KQ], vreg[VQ];
-    float ks_next = 0.0f, vs_next = 0.0f;
-    bool ok_next = false;
-    const int k_row = tid >> 2, k_off = (tid & 3) * (D / 4);
-    auto load = [&](int p) {
-        // where the table names no page, page 0 is read and nobody sees its keys
-        const int64_t id = batch_page(a.batch, b, p);
-        ok_next = id >= 0;
-        const int64_t at = (ok_next ? id : 0) * a.Hkv + hk;
-        const uint8_t *kp = a.k + at * (kPage * D), *vp = a.v + at * (kPage * D);
+    for (int n = 0; n < NC; n++) {
+        // rows past the last repeat it and are not stored
+        const int r = min(r0 + (wave * NC + n) * 32 + col, s.rows - 1);
+        const int i_tok = r / a.G;
+        lim[n] = visible(a, s, i_tok);
 #pragma unroll
-        for (int i = 0; i < KQ; i++) kreg[i] = *reinterpret_cast<const u32x4v *>(kp + k_row * D + k_off + 16 * i);
-#pragma unroll
-        for (int i = 0; i < VQ; i++) vreg[i] = *reinterpret_cast<const u32x4v *>(vp + 16 * (tid + 256 * i));
-        ks_next = a.k_scale[at];
-        vs_next = a.v_scale[at];
-    };
-    auto store = [&](int p, int buf, int slot) {
-        if ((p + 1) * kPage > lim_all) {                // some row does not see all of the page
-#pragma unroll
-            for (int i = 0; i < VQ; i++) {
-                const int u = tid + 256 * i, j = u & 3;
-                const int left = (int)s.kv - p * kPage - 16 * j;
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t x = vreg[i][w] & below_bytes(left - 4 * w);
-                    const uint32_t bad = nan_bytes(x);
-                    if (bad) {
-                        atomicOr(&nan_keys[slot][j >> 1], gather_bits(bad) << (16 * (j & 1) + 4 * w));
-                        x &= ~spread_bytes(bad);
-                    }
-                    vreg[i][w] = x;
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < KQ; i++) {
-            const int c = k_off / 8 + 2 * i;            // chunk in the key's row
-            const int sw = KC == 16 ? (k_row & 15) : ((k_row >> 1) & 7);
-            uint8_t *dst = ldsK[buf] + k_row * (2 * D);
-            *reinterpret_cast<u32x4v *>(dst + ((c ^ sw) << 4)) = widen8<DT>(kreg[i][0], kreg[i][1]);
-            *reinterpret_cast<u32x4v *>(dst + (((c + 1) ^ sw) << 4)) = widen8<DT>(kreg[i][2], kreg[i][3]);
-        }
-#pragma unroll
-        for (int i = 0; i < VQ; i++) {                  // 16 tokens of one dim: words 0, 2 for lanes 0-31, 1, 3 for 32-63
-            const int u = tid + 256 * i, d = u >> 2, j = u & 3;
-            const int sw = (d >> 1) & 7;
-            uint8_t *dst = ldsV[buf] + d * (2 * kPage);
-            *reinterpret_cast<u32x4v *>(dst + (((2 * j) ^ sw) << 4)) = widen8<DT>(vreg[i][0], vreg[i][2]);
-            *reinterpret_cast<u32x4v *>(dst + (((2 * j + 1) ^ sw) << 4)) = widen8<DT>(vreg[i][1], vreg[i][3]);
-        }
-    };
-
-    f32x16 o[D / 32];
-#pragma unroll
-    for (int d = 0; d < D / 32; d++)
-#pragma unroll
-        for (int e = 0; e < 16; e++) o[d][e] = 0.0f;
-    float m = kLow, l = 0.0f, vref = kMinScale;
-
-    if (tid < 6) (&nan_keys[0][0])[tid] = 0;
-    float ks = 0.0f, vs = 0.0f;
-    bool ok = false;
-    if (p0 < p1) {
-        load(p0);
-        __syncthreads();
-        store(p0, 0, 0);
-        ks = ks_next; vs = vs_next; ok = ok_next;
+        for (int k = 0; k < D / 16; k++)
+            q[n][k] = *reinterpret_cast<const u32x4v *>(a.q + (s.t0 + i_tok) * a.ld_q + (hk * a.G + (r - i_tok * a.G)) * D +
+                                                        16 * k + 8 * half);
     }
-    __syncthreads();
 
-    int slot = 0;
-    for (int p = p0; p < p1; p++) {
-        const int buf = (p - p0) & 1, slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
-        if (tid < 2) nan_keys[slot2][tid] = 0;          // read a page ago, written a page from now
-        const bool more = p + 1 < p1;
-        if (more) load(p + 1);
-
-        f32x16 sc[2];
+    // ---- staging: codes of a page in registers, then widened in LDS ----
+    // where the table names no page, page 0 is read and nobody sees its keys
+    auto page_of = [&](int32_t id, bool &ok) __attribute__((always_inline)) {
+        id = __builtin_amdgcn_readfirstlane(id);
+        ok = id >= 0 && id < a.batch.n_pages;
+        return (int64_t)(ok ? id : 0) * a.Hkv + hk;
+    };
+    // entry of page p in the table (p below the length, hence inside the table)
+    const int32_t *table = a.batch.table + (int64_t)b * a.batch.ld_table;
+    const int k_row = tid >> 2, k_off = (tid & 3) * (D / 4);
+    auto load_k = [&](int64_t at, u32x4v (&r)[KQ]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int kb = 0; kb < 2; kb++) {
+        for (int i = 0; i < KQ; i++)
+            r[i] = load_codes(a.k + at * (kPage * D), k_row * D + k_off + 16 * i);
+    };
+    auto load_v = [&](int64_t at, u32x4v (&r)[VQ]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 0; e < 16; e++) sc[kb][e] = 0.0f;
-            const int kr = 32 * kb + col;
-            const int sw = KC == 16 ? (kr & 15) : ((kr >> 1) & 7);
-            const uint8_t *src = ldsK[buf] + kr * (2 * D);
+        for (int i = 0; i < VQ; i++)
+            r[i] = load_codes(a.v + at * (kPage * D), 16 * (tid + 256 * i));
+    };
+    // the i-th of the 2 KQ 16-byte chunks that a thread widens of a tile
+    auto store_k = [&](const u32x4v (&r)[KQ], int buf, int i) __attribute__((always_inline)) {
+        *reinterpret_cast<u32x4v *>(ldsK[buf] + k_row * KROW + 2 * k_off + 16 * i) =
+            widen8<DT>(r[i >> 1][2 * (i & 1)], r[i >> 1][2 * (i & 1) + 1]);
+    };
+    auto store_v = [&](const u32x4v (&r)[VQ], int buf, int i) __attribute__((always_inline)) {
+        // 16 tokens of one dim: words 0, 2 for lanes 0-31, then 1, 3 for lanes 32-63
+        *reinterpret_cast<u32x4v *>(ldsV[buf] + ((tid >> 2) + 64 * (i >> 1)) * VROW + 32 * (tid & 3) + 16 * (i & 1)) =
+            widen8<1>(r[i >> 1][i & 1], r[i >> 1][2 + (i & 1)]);
+    };
+    // values of a page that some row does not see whole: nothing beyond the cache, NaN codes
+    // cleared and noted
+    auto clean_v = [&](u32x4v (&r)[VQ], int p) __attribute__((always_inline)) {
 #pragma unroll
-            for (int k = 0; k < D / 16; k++)
-                sc[kb] = Half<DT>::mfma32(*reinterpret_cast<const u32x4v *>(src + (((2 * k + half) ^ sw) << 4)), q[k], sc[kb]);
-        }
-        if ((p + 1) * kPage > lim_all || !ok) {         // masks: uniform in the workgroup
-            const int left = ok ? lim - p * kPage : 0;
+        for (int i = 0; i < VQ; i++) {
+            const int j = tid & 3;
+            const int left = s.kv - p * kPage - 16 * j;
 #pragma unroll
-            for (int kb = 0; kb < 2; kb++) {
-                const uint32_t bad = nan_keys[slot][kb];
-#pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const int key = 8 * (e >> 2) + 4 * half + (e & 3);
-                    const float x = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : sc[kb][e];
-                    sc[kb][e] = 32 * kb + key < left ? x : -__builtin_inff();
-                }
+            for (int w = 0; w < 4; w++) {
+                const uint32_t x = r[i][w] & below_bytes(left - 4 * w);
+                const uint32_t bad = nan_bytes(x);
+                if (bad) atomicOr(&nan_keys[p % 3][j >> 1], gather_bits(bad) << (16 * (j & 1) + 4 * w));
+                r[i][w] = x & ~spread_bytes(bad);
             }
         }
-        const float c = score_factor(a.factor, ks);
-        float mx = sc[0][0];
+    };
+
+    // ---- the parts of a page ----
+    f32x16 o[NC][D / 32];
+    float m[NC], l[NC], mx[NC], vref = kMinScale;
 #pragma unroll
-        for (int e = 1; e < 32; e++) mx = fmaxf(mx, sc[e >> 4][e & 15]);
-        mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
-        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
-            const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
-            m = m1;
-            l *= f;
+    for (int n = 0; n < NC; n++) {
+        m[n] = kLow;
+        l[n] = 0.0f;
 #pragma unroll
-            for (int d = 0; d < D / 32; d++)
+        for (int d = 0; d < D / 32; d++)
 #pragma unroll
-                for (int e = 0; e < 16; e++) o[d][e] *= f;
+            for (int e = 0; e < 16; e++) o[n][d][e] = 0.0f;
+    }
+    // operand i of the score products with 32 keys (half kb of a tile), of the second products
+    const int lane_k = col * KROW + 16 * half, lane_v = col * VROW + 16 * half;
+    auto read_k = [&](int buf, int kb, int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4v *>(ldsK[buf] + lane_k + 32 * kb * KROW + 32 * i);
+    };
+    auto read_v = [&](int buf, int kb, int i) __attribute__((always_inline)) {
+        const int j = i / (D / 32), d = i % (D / 32);
+        return *reinterpret_cast<const u32x4v *>(ldsV[buf] + lane_v + 32 * d * VROW + 32 * (2 * kb + j));
+    };
+    auto mask = [&](f32x16 (&x)[NC], int p, int kb, bool ok) __attribute__((always_inline)) {
+        const uint32_t bad = nan_keys[p % 3][kb] >> (4 * half);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+            const int left = (ok ? lim[n] - p * kPage : 0) - 32 * kb - 4 * half;
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+                const int key = 8 * (e >> 2) + (e & 3);
+                const float y = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : x[n][e];
+                x[n][e] = key < left ? y : -__builtin_inff();
+            }
         }
+    };
+    float top[NC];                                      // largest score of the half page so far
+    auto max_of = [&](const f32x16 (&x)[NC], int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NC; n++)
+#pragma unroll
+            for (int e = e0; e < e1; e++) top[n] = e == 0 ? x[n][0] : fmaxf(top[n], x[n][e]);
+#pragma unroll
+        for (int n = 0; n < NC; n++) stay(top[n]);
+    };
+    auto row_max = [&](float c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NC; n++) mx[n] = both_halves_max(top[n]) * c;
+    };
+    // the maximum of the scores about to be added: rescales what is there where it grows (rare)
+    auto raise = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NC; n++)
+            if (__builtin_amdgcn_ballot_w64(mx[n] > m[n] + kSlack) != 0) {
+                const float m1 = fmaxf(m[n], mx[n]), f = __builtin_amdgcn_exp2f(m[n] - m1);
+                m[n] = m1;
+                l[n] *= f;
+#pragma unroll
+                for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) o[n][d][e] *= f;
+            }
+    };
+    // the value scale of the page about to be added, likewise: its shift of the exponents and
+    // weight in the sum
+    float shift = 0.0f, weight = 1.0f;
+    auto take_scale = [&](float vs) __attribute__((always_inline)) {
         const float vsx = fmaxf(fmaxf(vs, kMinScale), vref * 0x1p-64f);
         if (vsx > vref) {                               // uniform
-            const float f = vref / vsx;
+            const float f = vref * __builtin_amdgcn_rcpf(vsx);
             vref = vsx;
+#pragma unroll
+            for (int n = 0; n < NC; n++)
+#pragma unroll
+                for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) o[n][d][e] *= f;
+        }
+        shift = __builtin_amdgcn_logf(vsx) - __builtin_amdgcn_logf(vref);
+        weight = vref * __builtin_amdgcn_rcpf(vsx);
+    };
+    u32x4v pk[NC][2];
+    float sum[NC];
+    auto softmax = [&](const f32x16 (&x)[NC], float c, int e0, int e1) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NC; n++)
+#pragma unroll
+            for (int e = e0; e < e1; e += 2) {
+                const float y = __builtin_amdgcn_exp2f(fmaf(x[n][e], c, shift - m[n]));
+                const float z = __builtin_amdgcn_exp2f(fmaf(x[n][e + 1], c, shift - m[n]));
+                sum[n] = e == 0 ? y + z : sum[n] + (y + z);
+                pk[n][e >> 3][(e >> 1) & 3] = Half<1>::pack(y, z);
+            }
+#pragma unroll
+        for (int n = 0; n < NC; n++) stay(sum[n]);
+    };
+    // A step: softmax of x (half kb of page p, tile bv of the values) and its second products;
+    // scores of the next half into y (half kb ^ 1 of tile bk of the keys); one tile's widening
+    // in quarters by `widen`; the first operands of the step after it (half kb of tile bk1).
+    // Written out in the order of issue: per matrix product the operand AHEAD of it is
+    // read, and as much vector work follows as the product takes.
+    constexpr int NQ = D / 16, NV = D / 16, AHEAD = 4, RING = 8;
+    u32x4v f[RING];
+    auto step = [&](int kb, const f32x16 (&x)[NC], f32x16 (&y)[NC], float c, int bk, int bv, int bk1,
+                    auto widen) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < NQ + NV; t++) {
+            const int u = t + AHEAD;
+            f[u % RING] = u < NQ ? read_k(bk, kb ^ 1, u) : u < NQ + NV ? read_v(bv, kb, u - NQ) : read_k(bk1, kb, u - NQ - NV);
+            if (t < NQ) {
+#pragma unroll
+                for (int n = 0; n < NC; n++) {
+                    if (t == 0)
+#pragma unroll
+                        for (int e = 0; e < 16; e++) y[n][e] = 0.0f;
+                    y[n] = Half<DT>::mfma32(f[t % RING], q[n][t], y[n]);
+                }
+                softmax(x, c, t * (16 / NQ), (t + 1) * (16 / NQ));
+            } else {
+                const int i = t - NQ;
+#pragma unroll
+                for (int n = 0; n < NC; n++) o[n][i % (D / 32)] = Half<1>::mfma32(f[t % RING], pk[n][i / (D / 32)], o[n][i % (D / 32)]);
+                if (i < NV / 2) widen(i);
+                else max_of(y, (i - NV / 2) * (32 / NV), (i - NV / 2 + 1) * (32 / NV));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int n = 0; n < NC; n++) l[n] = fmaf(sum[n], weight, l[n]);
+    };
+
+    if (tid < 6) (&nan_keys[0][0])[tid] = 0;
+    __syncthreads();
+    if (p0 < p1) {
+        u32x4v kr[KQ], vr[VQ];
+        auto masked = [&](int p, bool ok) __attribute__((always_inline)) { return (p + 1) * kPage > lim_all || !ok; };
+        const int pl = p1 - 1;                          // the last page stands in where there is none (never used)
+        // pages p, p + 1, p + 2: where they are, and the scales of the first two
+        bool ok, ok1, ok2;
+        int64_t at = page_of(table[p0], ok), at1 = page_of(table[min(p0 + 1, pl)], ok1);
+        int64_t at2 = page_of(table[min(p0 + 2, pl)], ok2);
+        int32_t id3 = table[min(p0 + 3, pl)];
+        float c = score_factor(a.factor, a.k_scale[at]), vs = a.v_scale[at];
+        float ks1 = a.k_scale[at1], vs1 = a.v_scale[at1];
+        f32x16 sa[NC], sb[NC];
+        {
+            u32x4v k0[KQ], v0[VQ], k1[KQ];              // all in flight together
+            load_k(at, k0);
+            load_v(at, v0);
+            load_k(at1, k1);
+            load_v(at1, vr);
+            if (masked(p0, ok)) clean_v(v0, p0);
+#pragma unroll
+            for (int i = 0; i < 2 * KQ; i++) {
+                store_k(k0, 0, i);
+                store_v(v0, 0, i);
+                store_k(k1, 1, i);
+            }
+        }
+        load_k(at2, kr);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+#pragma unroll
+            for (int e = 0; e < 16; e++) sa[n][e] = 0.0f;
+#pragma unroll
+            for (int t = 0; t < NQ; t++) sa[n] = Half<DT>::mfma32(read_k(0, 0, t), q[n][t], sa[n]);
+        }
+        if (masked(p0, ok)) mask(sa, p0, 0, ok);
+        max_of(sa, 0, 16);
+        row_max(c);
+#pragma unroll
+        for (int t = 0; t < AHEAD; t++) f[t] = read_k(0, 1, t);
+        for (int p = p0; p < pl; p++) {
+            const int cur = (p - p0) & 1, nxt = cur ^ 1;
+            // ---- keys 0..31 of page p; the scores of its keys 32..63; values p + 1 staged ----
+            take_scale(vs);
+            raise();
+            if (masked(p + 1, ok1)) {
+                clean_v(vr, p + 1);
+                __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): its notes are written
+            }
+            barrier_but<AHEAD>();                       // values p are staged; values p - 1 are read
+            if (tid < 2) nan_keys[(p + 2) % 3][tid] = 0;       // read in page p - 1, written after the next barrier
+            step(0, sa, sb, c, cur, cur, nxt, [&](int i) __attribute__((always_inline)) { store_v(vr, nxt, i); });
+            load_v(at2, vr);
+            if (masked(p, ok)) {
+                mask(sb, p, 1, ok);
+                max_of(sb, 0, 16);
+            }
+            row_max(c);
+            raise();
+            barrier_but<AHEAD>();                       // keys p + 1 are staged; keys p are read
+            // ---- keys 32..63; the scores of keys 0..31 of page p + 1; keys p + 2 staged ----
+            step(1, sb, sa, c, nxt, cur, nxt, [&](int i) __attribute__((always_inline)) { store_k(kr, cur, i); });
+            ok = ok1;
+            c = score_factor(a.factor, ks1);
+            vs = vs1;
+            if (masked(p + 1, ok)) {
+                mask(sa, p + 1, 0, ok);
+                max_of(sa, 0, 16);
+            }
+            row_max(c);
+            ks1 = a.k_scale[at2];
+            vs1 = a.v_scale[at2];
+            ok1 = ok2;
+            at2 = page_of(id3, ok2);
+            id3 = table[min(p + 4, pl)];
+            load_k(at2, kr);
+        }
+        // ---- the last page ----
+        const int cur = (pl - p0) & 1;
+        take_scale(vs);
+        raise();
+        __syncthreads();
+        step(0, sa, sb, c, cur, cur, cur, [](int) {});
+        if (masked(pl, ok)) {
+            mask(sb, pl, 1, ok);
+            max_of(sb, 0, 16);
+        }
+        row_max(c);
+        raise();
+        softmax(sb, c, 0, 16);
+#pragma unroll
+        for (int n = 0; n < NC; n++) l[n] = fmaf(sum[n], weight, l[n]);
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int n = 0; n < NC; n++)
+                o[n][i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[n][i / (D / 32)], o[n][i % (D / 32)]);
+    }
+
+    // ---- the lane's rows (found again rather than kept): dims 32 d + 8 g + 4 half + 0..3 ----
+#pragma unroll
+    for (int n = 0; n < NC; n++) {
+        const float total = l[n] + __shfl_xor(l[n], 32);
+        const int r = r0 + opaque_lane((wave * NC + n) * 32 + col);
+        if (r >= s.rows) continue;
+        const int64_t row = s.t0 + r / a.G;
+        const int head = hk * a.G + r % a.G;
+        if (a.splits > 1) {
+            float *po = a.part_o + (((int64_t)split * a.batch.T + row) * a.Hq + head) * D;
 #pragma unroll
             for (int d = 0; d < D / 32; d++)
 #pragma unroll
-                for (int e = 0; e < 16; e++) o[d][e] *= f;
+                for (int g = 0; g < 4; g++)
+                    *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
+                        f32x4{o[n][d][4 * g] * vref, o[n][d][4 * g + 1] * vref, o[n][d][4 * g + 2] * vref,
+                              o[n][d][4 * g + 3] * vref};
+            if (half == 0) a.part_ml[((int64_t)split * a.batch.T + row) * a.Hq + head] = float2{m[n], total};
+            continue;
         }
-        const float shift = __builtin_amdgcn_logf(vsx / vref) - m;
-        float sum = 0.0f;
-        u32x4v pk[4];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 4][e & 15], c, shift));
-            const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 4][(e & 15) + 1], c, shift));
-            sum += x + y;
-            pk[e >> 3][(e >> 1) & 3] = Half<DT>::pack(x, y);
-        }
-        l = fmaf(sum, vref / vsx, l);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-#pragma unroll
-            for (int d = 0; d < D / 32; d++) {
-                const int vr = 32 * d + col;
-                const uint8_t *src = ldsV[buf] + vr * (2 * kPage) + (((2 * j + half) ^ ((vr >> 1) & 7)) << 4);
-                o[d] = Half<DT>::mfma32(*reinterpret_cast<const u32x4v *>(src), pk[j], o[d]);
-            }
-        if (more) {
-            store(p + 1, buf ^ 1, slot1);
-            ks = ks_next; vs = vs_next; ok = ok_next;
-        }
-        slot = slot1;
-        __syncthreads();
-    }
-
-    // ---- the lane's row: dims 32 d + 8 g + 4 half + 0..3 ----
-    l += __shfl_xor(l, 32);
-    if (!valid) return;
-    if (a.splits > 1) {
-        float *po = a.part_o + (((int64_t)split * a.batch.T + row) * a.Hq + head) * D;
+        const float inv = total == 0.0f ? 0.0f : vref / total;
+        uint16_t *po = a.out + row * a.ld_out + (int64_t)head * D;
 #pragma unroll
         for (int d = 0; d < D / 32; d++)
 #pragma unroll
             for (int g = 0; g < 4; g++)
-                *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
-                    f32x4{o[d][4 * g] * vref, o[d][4 * g + 1] * vref, o[d][4 * g + 2] * vref, o[d][4 * g + 3] * vref};
-        if (half == 0) a.part_ml[((int64_t)split * a.batch.T + row) * a.Hq + head] = float2{m, l};
-        return;
+                *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
+                    u32x2v{Half<DT>::pack(o[n][d][4 * g] * inv, o[n][d][4 * g + 1] * inv),
+                           Half<DT>::pack(o[n][d][4 * g + 2] * inv, o[n][d][4 * g + 3] * inv)};
     }
-    const float inv = l == 0.0f ? 0.0f : vref / l;
-    uint16_t *po = a.out + row * a.ld_out + (int64_t)head * D;
-#pragma unroll
-    for (int d = 0; d < D / 32; d++)
-#pragma unroll
-        for (int g = 0; g < 4; g++)
-            *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
-                u32x2v{Half<DT>::pack(o[d][4 * g] * inv, o[d][4 * g + 1] * inv),
-                       Half<DT>::pack(o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv)};
 }
 
 // ------------------------------------------------------------- single tokens: few rows ----
@@ -402,19 +580,17 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
     const int block = rest % a.row_blocks, split = rest / a.row_blocks;
     const int b = unit / a.Hkv, hk = unit % a.Hkv;
     const Seq s = load_seq(a, b);
-    const int64_t r0 = (int64_t)block * kFewRows;
+    const int r0 = block * kFewRows;
     if (r0 >= s.rows) return;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quarter = lane >> 4;
-    const int64_t r = r0 + col;
-    const bool valid = r < s.rows;
-    const int64_t i_tok = valid ? r / a.G : 0;
-    const int head = hk * a.G + (valid ? (int)(r - i_tok * a.G) : 0);
-    const int64_t last = (r0 + kFewRows < s.rows ? r0 + kFewRows : s.rows) - 1;
-    const int lim = valid ? (int)visible(a, s, i_tok) : 0;
-    const int lim_all = (int)visible(a, s, r0 / a.G);
-    const int pages = ((int)visible(a, s, last / a.G) + kPage - 1) / kPage;
+    const int r = min(r0 + col, s.rows - 1);             // rows past the last repeat it and are not stored
+    const int i_tok = r / a.G, head = hk * a.G + (r - i_tok * a.G);
+    const int last = min(r0 + kFewRows, s.rows) - 1;
+    const int lim = visible(a, s, i_tok);
+    const int lim_all = visible(a, s, r0 / a.G);
+    const int pages = (visible(a, s, last / a.G) + kPage - 1) / kPage;
     const int p0 = (int)(split * a.pages_per_split);
     const int p1 = split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
     if (a.splits > 1 && p0 >= p1) return;
@@ -425,9 +601,8 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
     for (int c = 0; c < C; c++)
 #pragma unroll
         for (int u = 0; u < 2; u++)
-            q[c][u] = valid ? *reinterpret_cast<const u32x4v *>(a.q + (s.t0 + i_tok) * a.ld_q + (int64_t)head * D +
-                                                                 64 * c + 16 * quarter + 8 * u)
-                            : u32x4v{0u, 0u, 0u, 0u};
+            q[c][u] = *reinterpret_cast<const u32x4v *>(a.q + (s.t0 + i_tok) * a.ld_q + head * D + 64 * c +
+                                                        16 * quarter + 8 * u);
 
     f32x4 o[D / 16];
 #pragma unroll
@@ -462,7 +637,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
         }
         if ((p + 1) * kPage > lim_all) {                 // some row does not see all of the page
             uint32_t bad = 0;                            // this lane's 16 keys whose values hold NaN codes
-            const int inside = (int)s.kv - p * kPage - 16 * quarter;
+            const int inside = s.kv - p * kPage - 16 * quarter;
 #pragma unroll
             for (int d = 0; d < D / 16; d++)
 #pragma unroll
@@ -512,13 +687,13 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
             const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], c, shift));
             const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][(e & 3) + 1], c, shift));
             sum += x + y;
-            pk[e >> 3][(e >> 1) & 3] = Half<DT>::pack(x, y);
+            pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(x, y);
         }
         l = fmaf(sum, vref / vsx, l);
 #pragma unroll
         for (int d = 0; d < D / 16; d++) {
-            o[d] = Half<DT>::mfma16(widen8<DT>(vr[d][0], vr[d][1]), pk[0], o[d]);
-            o[d] = Half<DT>::mfma16(widen8<DT>(vr[d][2], vr[d][3]), pk[1], o[d]);
+            o[d] = Half<1>::mfma16(widen8<1>(vr[d][0], vr[d][1]), pk[0], o[d]);
+            o[d] = Half<1>::mfma16(widen8<1>(vr[d][2], vr[d][3]), pk[1], o[d]);
         }
     }
 
@@ -531,7 +706,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
             f32x4{o[d][0] * vref, o[d][1] * vref, o[d][2] * vref, o[d][3] * vref};
     if (quarter == 0) { lm[wave][col] = m; ll[wave][col] = l; }
     __syncthreads();
-    const int n_rows = (int)(last - r0) + 1;
+    const int n_rows = last - r0 + 1;
     for (int i = tid; i < n_rows * (D / 2); i += 256) {
         const int rr = i / (D / 2), d = 2 * (i % (D / 2));
         float top = kLow, x = 0.0f, y = 0.0f, sum = 0.0f;
@@ -544,8 +719,8 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
             y = fmaf(lo[w][rr][d + 1], f, y);
             sum = fmaf(ll[w][rr], f, sum);
         }
-        const int64_t gr = r0 + rr, tok = gr / a.G;
-        const int hd = hk * a.G + (int)(gr - tok * a.G);
+        const int gr = r0 + rr, tok = gr / a.G;
+        const int hd = hk * a.G + (gr - tok * a.G);
         if (a.splits > 1) {
             const int64_t at = ((int64_t)split * a.batch.T + s.t0 + tok) * a.Hq + hd;
             *reinterpret_cast<float2 *>(a.part_o + at * D + d) = float2{x, y};
@@ -573,8 +748,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
         if (b + step < a.B && a.batch.cu[b + step] <= row) b += step;
     const Seq s = load_seq(a, b);
     if (row < s.t0 || row >= s.t0 + s.n) return;         // a row of no sequence
-    const int lim = (int)visible(a, s, row - s.t0);
-    const int64_t pages = (lim + kPage - 1) / kPage;
+    const int64_t pages = (visible(a, s, (int)(row - s.t0)) + kPage - 1) / kPage;
     int64_t n = (pages + a.pages_per_split - 1) / a.pages_per_split;
     if (n > a.splits) n = a.splits;
     const int64_t stride = a.batch.T * a.Hq;
@@ -598,6 +772,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
 }
 
 // ----------------------------------------------------------------------- launching ----
+
+constexpr int kRowBlocks = 1, kRowsBlock = 32 * kWaves * kRowBlocks;
 
 AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int Hq, int Hkv, int D, int cus)
 {
@@ -630,7 +806,7 @@ static hipError_t launch_attn(const AttnArgs &a, bool few, hipStream_t st)
     const int64_t blocks = (int64_t)a.B * a.Hkv * a.row_blocks * a.splits;
     if (blocks > (int64_t)(UINT32_MAX / 256)) return hipErrorInvalidValue;
     if (few) hipLaunchKernelGGL((attn_few_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((attn_rows_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((attn_rows_kernel<DT, D, kRowBlocks>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3((unsigned)((a.batch.T * a.Hq + 3) / 4)), dim3(256), 0, st, a);
