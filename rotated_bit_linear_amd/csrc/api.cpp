@@ -1090,9 +1090,9 @@ cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, in
         if (ws_bytes < p.bytes) return CR_ERR_TOO_LARGE;
     }
     if (!any || max_q == 0) return CR_OK;
-    // workgroups of 256 threads; a dispatch counts work-items in 32 bits
-    const int64_t most = (int64_t)(UINT32_MAX / 256);
-    if (B > most / Hkv / p.row_blocks / p.splits || T > 4 * most / Hq) return CR_ERR_TOO_LARGE;
+    if (p.whole > convrot::kMostBlocks || p.whole + p.tail * p.splits > convrot::kMostBlocks ||
+        T > 4 * convrot::kMostBlocks / Hq)
+        return CR_ERR_TOO_LARGE;
     if ((s = current_device_ok()) != CR_OK) return s;
     convrot::AttnLaunch l{};
     l.q = q; l.dtype = (int)dtype; l.ld_q = ld_q; l.out = out; l.ld_out = ld_out; l.T = T; l.B = B;

@@ -50,12 +50,13 @@ struct AttnArgs {
     const float *k_scale, *v_scale;
     Batch batch;
     int B, Hq, Hkv, G;       // G = Hq / Hkv
-    int row_blocks, splits;
+    int row_blocks;          // blocks of query rows a sequence and key/value head
+    int whole, tail, splits; // blocks done by one workgroup each, then blocks split into runs of pages
     int64_t pages_per_split;
     float factor;            // sm_scale * log2(e)
     int causal;
-    float *part_o;           // [split][T][Hq][D], times 2^(m) sums of p v (splits > 1)
-    float2 *part_ml;         // [split][T][Hq] (running maximum, sum)
+    float *part_o;           // of each split block [split][tail][rows of a block][D]: sums of p v
+    float2 *part_ml;         // [split][tail][rows of a block] (running maximum, sum)
 };
 
 // 16-bit operand types: bf16 (0) or fp16 (1)
@@ -185,6 +186,30 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b)
     s.rows = s.n * a.G;
     return s;
 }
+// what a workgroup does: block `block` of the rows of sequence b and key/value head hk; the whole
+// cache (split < 0), or its run `split` (part: where that goes)
+struct Task {
+    int b, hk, block, split, part;
+};
+// Key/value heads lie apart by the XCDs' stride; the longest rows (causal) come first.
+__device__ __forceinline__ Task task_of(const AttnArgs &a, int id)
+{
+    Task t;
+    t.split = -1;
+    t.part = 0;
+    int w = id;
+    if (id >= a.whole) {
+        t.part = id - a.whole;
+        t.split = t.part / a.tail;
+        w = a.whole + t.part % a.tail;
+    }
+    const int units = a.B * a.Hkv, unit = w % units;
+    t.block = a.row_blocks - 1 - w / units;
+    t.b = unit / a.Hkv;
+    t.hk = unit % a.Hkv;
+    return t;
+}
+
 // number of keys that token i of the sequence sees
 __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 {
@@ -204,7 +229,7 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 constexpr int kWaves = 4;
 
 template <int DT, int D, int NC>
-__global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArgs a)
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArgs a)
 {
     constexpr int KROW = 2 * D + 16, VROW = 2 * kPage + 16;   // bytes of a widened row of keys, of values
     constexpr int KQ = D / 64, VQ = D / 64;             // 16-byte code loads a thread and tile
@@ -213,26 +238,24 @@ __global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArg
     __shared__ __attribute__((aligned(16))) uint8_t ldsV[2][D * VROW];
     __shared__ uint32_t nan_keys[3][2];                 // keys of a tile whose values hold NaN codes
 
-    // longest rows first (causal), key/value heads apart by the XCDs' stride
-    const int units = a.B * a.Hkv;
-    const int unit = blockIdx.x % units, rest = blockIdx.x / units;
-    const int split = rest % a.splits, block = a.row_blocks - 1 - rest / a.splits;
-    const int b = unit / a.Hkv, hk = unit % a.Hkv;
+    const Task task = task_of(a, blockIdx.x);
+    const int b = task.b, hk = task.hk;
     const Seq s = load_seq(a, b);
-    const int r0 = block * ROWS;
+    const int r0 = task.block * ROWS;
     if (r0 >= s.rows) return;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
 
     // keys seen by this lane's rows, by the block's last row (the loop's end) and by all of its rows
     const int last = min(r0 + ROWS, s.rows) - 1;
     const int lim_all = visible(a, s, r0 / a.G);
     const int pages = (visible(a, s, last / a.G) + kPage - 1) / kPage;
-    const int p0 = (int)(split * a.pages_per_split);
-    const int p1 = split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
-    if (a.splits > 1 && p0 >= p1) return;               // no row of the block looks here
+    const int p0 = task.split < 0 ? 0 : (int)(task.split * a.pages_per_split);
+    const int p1 = task.split < 0 || task.split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
+    if (task.split >= 0 && p0 >= p1) return;               // no row of the block looks here
 
+    const bool busy = r0 + wave * NC * 32 < s.rows;     // a wave without rows only stages
     int lim[NC];
     u32x4v q[NC][D / 16];
 #pragma unroll
@@ -393,10 +416,15 @@ __global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArg
     // in quarters by `widen`; the first operands of the step after it (half kb of tile bk1).
     // Written out in the order of issue: per matrix product the operand AHEAD of it is
     // read, and as much vector work follows as the product takes.
-    constexpr int NQ = D / 16, NV = D / 16, AHEAD = 4, RING = 8;
+    constexpr int NQ = D / 16, NV = D / 16, AHEAD = D == 64 ? 3 : 4, RING = D == 64 ? 4 : 8;
     u32x4v f[RING];
     auto step = [&](int kb, const f32x16 (&x)[NC], f32x16 (&y)[NC], float c, int bk, int bv, int bk1,
                     auto widen) __attribute__((always_inline)) {
+        if (!busy) {                                    // uniform in the wave
+#pragma unroll
+            for (int i = 0; i < NV / 2; i++) widen(i);
+            return;
+        }
 #pragma unroll
         for (int t = 0; t < NQ + NV; t++) {
             const int u = t + AHEAD;
@@ -530,10 +558,9 @@ __global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArg
         const float total = l[n] + __shfl_xor(l[n], 32);
         const int r = r0 + opaque_lane((wave * NC + n) * 32 + col);
         if (r >= s.rows) continue;
-        const int64_t row = s.t0 + r / a.G;
-        const int head = hk * a.G + r % a.G;
-        if (a.splits > 1) {
-            float *po = a.part_o + (((int64_t)split * a.batch.T + row) * a.Hq + head) * D;
+        if (task.split >= 0) {
+            const int64_t at = (int64_t)task.part * ROWS + (r - r0);
+            float *po = a.part_o + at * D;
 #pragma unroll
             for (int d = 0; d < D / 32; d++)
 #pragma unroll
@@ -541,11 +568,11 @@ __global__ __launch_bounds__(256, NC == 2 ? 1 : 2) void attn_rows_kernel(AttnArg
                     *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
                         f32x4{o[n][d][4 * g] * vref, o[n][d][4 * g + 1] * vref, o[n][d][4 * g + 2] * vref,
                               o[n][d][4 * g + 3] * vref};
-            if (half == 0) a.part_ml[((int64_t)split * a.batch.T + row) * a.Hq + head] = float2{m[n], total};
+            if (half == 0) a.part_ml[at] = float2{m[n], total};
             continue;
         }
         const float inv = total == 0.0f ? 0.0f : vref / total;
-        uint16_t *po = a.out + row * a.ld_out + (int64_t)head * D;
+        uint16_t *po = a.out + (s.t0 + r / a.G) * a.ld_out + (hk * a.G + r % a.G) * D;
 #pragma unroll
         for (int d = 0; d < D / 32; d++)
 #pragma unroll
@@ -575,12 +602,10 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
     __shared__ float lo[4][kFewRows][D + 4];
     __shared__ float lm[4][kFewRows], ll[4][kFewRows];
 
-    const int units = a.B * a.Hkv;
-    const int unit = blockIdx.x % units, rest = blockIdx.x / units;
-    const int block = rest % a.row_blocks, split = rest / a.row_blocks;
-    const int b = unit / a.Hkv, hk = unit % a.Hkv;
+    const Task task = task_of(a, blockIdx.x);
+    const int b = task.b, hk = task.hk;
     const Seq s = load_seq(a, b);
-    const int r0 = block * kFewRows;
+    const int r0 = task.block * kFewRows;
     if (r0 >= s.rows) return;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -591,9 +616,9 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
     const int lim = visible(a, s, i_tok);
     const int lim_all = visible(a, s, r0 / a.G);
     const int pages = (visible(a, s, last / a.G) + kPage - 1) / kPage;
-    const int p0 = (int)(split * a.pages_per_split);
-    const int p1 = split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
-    if (a.splits > 1 && p0 >= p1) return;
+    const int p0 = task.split < 0 ? 0 : (int)(task.split * a.pages_per_split);
+    const int p1 = task.split < 0 || task.split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
+    if (task.split >= 0 && p0 >= p1) return;
 
     // queries: dims 64 c + 16 quarter + 8 u ..
     u32x4v q[C][2];
@@ -721,8 +746,8 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
         }
         const int gr = r0 + rr, tok = gr / a.G;
         const int hd = hk * a.G + (gr - tok * a.G);
-        if (a.splits > 1) {
-            const int64_t at = ((int64_t)split * a.batch.T + s.t0 + tok) * a.Hq + hd;
+        if (task.split >= 0) {
+            const int64_t at = (int64_t)task.part * kFewRows + rr;
             *reinterpret_cast<float2 *>(a.part_o + at * D + d) = float2{x, y};
             if (d == 0) a.part_ml[at] = float2{top, sum};
         } else {
@@ -734,39 +759,37 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
 }
 
 // --------------------------------------------------------------- joining the splits ----
-// One wave per query row: the runs that hold keys the row sees, in order.
+// One wave per row of the split blocks: the runs that hold keys the row sees, in order.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a)
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t rid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (rid >= a.batch.T * a.Hq) return;
-    const int64_t row = rid / a.Hq;
-    // the sequence of this row (the rows of sequence b start at cu[b])
-    int b = 0;
-    for (int step = 1 << 30; step > 0; step >>= 1)
-        if (b + step < a.B && a.batch.cu[b + step] <= row) b += step;
-    const Seq s = load_seq(a, b);
-    if (row < s.t0 || row >= s.t0 + s.n) return;         // a row of no sequence
-    const int64_t pages = (visible(a, s, (int)(row - s.t0)) + kPage - 1) / kPage;
-    int64_t n = (pages + a.pages_per_split - 1) / a.pages_per_split;
-    if (n > a.splits) n = a.splits;
-    const int64_t stride = a.batch.T * a.Hq;
+    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t stride = (int64_t)a.tail * rows;       // rows of one split
+    if (id >= stride) return;
+    const Task task = task_of(a, a.whole + (int)(id / rows));
+    const Seq s = load_seq(a, task.b);
+    const int r = task.block * rows + (int)(id % rows);
+    if (r >= s.rows) return;
+    const int tok = r / a.G;
+    const int64_t pages = (visible(a, s, tok) + kPage - 1) / kPage;
+    const int n = (int)min((pages + a.pages_per_split - 1) / a.pages_per_split, (int64_t)a.splits);
     float top = kLow;
-    for (int64_t i = lane; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + rid].x);
+    for (int i = lane; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + id].x);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
     constexpr int E = D / 64;
     float acc[E] = {}, sum = 0.0f;
-    for (int64_t i = 0; i < n; i++) {
-        const float2 ml = a.part_ml[i * stride + rid];
+#pragma unroll 4
+    for (int i = 0; i < n; i++) {
+        const float2 ml = a.part_ml[i * stride + id];
         const float f = __builtin_amdgcn_exp2f(ml.x - top);
         sum = fmaf(ml.y, f, sum);
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(a.part_o[(i * stride + rid) * D + E * lane + e], f, acc[e]);
+        for (int e = 0; e < E; e++) acc[e] = fmaf(a.part_o[(i * stride + id) * D + E * lane + e], f, acc[e]);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *po = a.out + row * a.ld_out + (rid - row * a.Hq) * D + E * lane;
+    uint16_t *po = a.out + (s.t0 + tok) * a.ld_out + (task.hk * a.G + (r - tok * a.G)) * D + E * lane;
     if constexpr (E == 2) *reinterpret_cast<uint32_t *>(po) = Half<DT>::pack(acc[0] * inv, acc[1] * inv);
     else *po = (uint16_t)Half<DT>::pack(acc[0] * inv, 0.0f);
 }
@@ -785,31 +808,62 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     const int per = p.few ? kFewRows : kRowsBlock;
     p.row_blocks = (rows + per - 1) / per;
     const int64_t pages = max_kv > 0 ? (max_kv + kPage - 1) / kPage : 1;
+    if (B > kMostBlocks / Hkv / p.row_blocks) {          // more than a launch counts: refused by the caller
+        p.whole = kMostBlocks + 1;
+        return p;
+    }
     const int64_t base = B * Hkv * p.row_blocks;
-    // workgroups wanted, and the fewest pages that are worth one
-    const int64_t want = (p.few ? 8 : 2) * (int64_t)cus, least = p.few ? 4 : 8;
-    int64_t splits = (want + base - 1) / base;
-    if (splits > pages / least) splits = pages / least;
-    if (splits < 1) splits = 1;
-    p.pages_per_split = (pages + splits - 1) / splits;
-    p.splits = (pages + p.pages_per_split - 1) / p.pages_per_split;
-    if (p.splits > 1) {
-        p.off_ml = (((size_t)p.splits * (size_t)T * Hq * D * 4) + 255) & ~(size_t)255;
-        p.bytes = p.off_ml + (size_t)p.splits * (size_t)T * Hq * 8;
+    p.whole = base;
+    if (p.few) {
+        // eight workgroups a compute unit, of at least a page a wave
+        int64_t n = (8 * (int64_t)cus + base - 1) / base;
+        if (n > pages / 4) n = pages / 4;
+        if (n > 1) {
+            p.whole = 0;
+            p.splits = n;
+        }
+    } else {
+        // Rounds of workgroups over the device, each as long as its pages and a start worth three.
+        // Either every block is split, or only those left over by whole rounds (the device then
+        // shares them out).  The FP32 parts are written and read: in the time of a page the device
+        // moves about 10 KiB a compute unit.
+        const int64_t slots = (D == 64 ? 3 : 2) * (int64_t)cus;
+        int64_t best = (base + slots - 1) / slots * (pages + 3) * 95 / 100;   // splitting has to save 5 %
+        for (const int64_t whole : {(int64_t)0, base / slots * slots}) {
+            const int64_t tail = base - whole;
+            if (tail == 0) continue;
+            for (int64_t n = 2; n <= pages / 8 && n <= 64; n++) {
+                const int64_t join = 2 * n * tail * kRowsBlock * D * 4 / (10240 * (int64_t)cus);
+                const int64_t cost = whole / slots * (pages + 3) + (tail * n + slots - 1) / slots * ((pages + n - 1) / n + 3) + join;
+                if (cost < best) {
+                    best = cost;
+                    p.whole = whole;
+                    p.splits = n;
+                }
+            }
+        }
+    }
+    p.tail = base - p.whole;
+    if (p.tail > 0) {
+        p.pages_per_split = (pages + p.splits - 1) / p.splits;
+        p.splits = (pages + p.pages_per_split - 1) / p.pages_per_split;
+        p.off_ml = (size_t)p.splits * (size_t)p.tail * per * D * 4;
+        p.bytes = p.off_ml + (size_t)p.splits * (size_t)p.tail * per * 8;
     }
     return p;
 }
 
 template <int DT, int D>
-static hipError_t launch_attn(const AttnArgs &a, bool few, hipStream_t st)
+static hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, hipStream_t st)
 {
-    const int64_t blocks = (int64_t)a.B * a.Hkv * a.row_blocks * a.splits;
-    if (blocks > (int64_t)(UINT32_MAX / 256)) return hipErrorInvalidValue;
-    if (few) hipLaunchKernelGGL((attn_few_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    const int64_t blocks = p.whole + p.tail * p.splits;
+    if (blocks > kMostBlocks) return hipErrorInvalidValue;
+    if (p.few) hipLaunchKernelGGL((attn_few_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     else hipLaunchKernelGGL((attn_rows_kernel<DT, D, kRowBlocks>), dim3((unsigned)blocks), dim3(256), 0, st, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3((unsigned)((a.batch.T * a.Hq + 3) / 4)), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.tail == 0) return e;
+    const int rows = p.few ? kFewRows : kRowsBlock;
+    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3((unsigned)((p.tail * rows + 3) / 4)), dim3(256), 0, st, a, rows);
     return hipGetLastError();
 }
 
@@ -822,14 +876,15 @@ hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st)
     a.k = l.cache.k; a.v = l.cache.v; a.k_scale = l.cache.k_scale; a.v_scale = l.cache.v_scale;
     a.batch = Batch{l.cu, l.kv_lens, l.cache.table, l.cache.ld_table, l.cache.n_pages, l.T};
     a.B = (int)l.B; a.Hq = l.Hq; a.Hkv = l.Hkv; a.G = l.Hq / l.Hkv;
-    a.row_blocks = (int)l.plan.row_blocks; a.splits = (int)l.plan.splits;
+    a.row_blocks = (int)l.plan.row_blocks;
+    a.whole = (int)l.plan.whole; a.tail = (int)l.plan.tail; a.splits = (int)l.plan.splits;
     a.pages_per_split = l.plan.pages_per_split;
     a.factor = l.sm_scale * 1.4426950408889634f;
     a.causal = l.causal;
     a.part_o = static_cast<float *>(l.workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(l.workspace) + l.plan.off_ml);
-    if (l.D == 128) return l.dtype == 0 ? launch_attn<0, 128>(a, l.plan.few, st) : launch_attn<1, 128>(a, l.plan.few, st);
-    return l.dtype == 0 ? launch_attn<0, 64>(a, l.plan.few, st) : launch_attn<1, 64>(a, l.plan.few, st);
+    if (l.D == 128) return l.dtype == 0 ? launch_attn<0, 128>(a, l.plan, st) : launch_attn<1, 128>(a, l.plan, st);
+    return l.dtype == 0 ? launch_attn<0, 64>(a, l.plan, st) : launch_attn<1, 64>(a, l.plan, st);
 }
 
 }  // namespace convrot

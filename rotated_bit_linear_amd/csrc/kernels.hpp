@@ -118,14 +118,17 @@ struct RopeLaunch {
 };
 hipError_t launch_rope_append_kv8(const RopeLaunch &r, hipStream_t st);
 
-// attention over the cache: which kernel runs and how the cache is split (attn_kv8.hip)
+// attention over the cache: which kernel runs and how the work is split (attn_kv8.hip).  A block is
+// a run of query rows of one sequence and key/value head.
 struct AttnPlan {
-    bool few;                // few query rows a kv head: one wave holds them all
-    int64_t row_blocks;      // blocks of query rows a sequence and kv head
-    int64_t pages_per_split;
-    int64_t splits;          // 1: the kernel writes the output itself
-    size_t off_ml, bytes;    // workspace: partial outputs, then (maximum, sum) pairs
+    bool few;                // few query rows a kv head: one wave holds a block's
+    int64_t row_blocks;      // blocks a sequence and kv head
+    int64_t whole, tail;     // blocks that one workgroup does, and blocks split over the cache
+    int64_t splits, pages_per_split;
+    size_t off_ml, bytes;    // workspace of the split blocks: partial outputs, then (maximum, sum) pairs
 };
+// workgroups of 256 threads that a dispatch's 32-bit work-item count allows
+constexpr int64_t kMostBlocks = (int64_t)(UINT32_MAX / 256);
 AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int Hq, int Hkv, int D, int cus);
 
 struct AttnLaunch {
