@@ -1047,9 +1047,10 @@ cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, in
         return CR_ERR_MISALIGNED;
     if (max_new > T) max_new = T;
     if (!any || max_new == 0) return CR_OK;
-    // workgroups of 256 threads, at most one per page visited and head; a dispatch counts work-items in 32 bits
+    // workgroups of at most 512 threads, at most one per page visited and head; a dispatch counts
+    // work-items in 32 bits
     const int64_t visits = (max_new + CR_KV8_PAGE - 2) / CR_KV8_PAGE + 1;
-    if (B > (int64_t)(UINT32_MAX / 256) / visits / (Hq + Hkv)) return CR_ERR_TOO_LARGE;
+    if (B > (int64_t)(UINT32_MAX / 512) / visits / (Hq + Hkv)) return CR_ERR_TOO_LARGE;
     if ((s = current_device_ok()) != CR_OK) return s;
     convrot::RopeLaunch r{};
     r.qkv = qkv; r.dtype = (int)dtype; r.ld_qkv = ld_qkv; r.q_out = q_out; r.ld_q = ld_q;

@@ -239,6 +239,26 @@ def test_non_finite_values_leave_the_others():
         assert torch.equal(av, bv)
 
 
+def test_infinite_values_are_nan_codes():
+    """Infinities of both signs in a key and in values: NaN codes there, the page's scale from the rest."""
+    batch = Batch([3], [3], seed=18)
+    cache = random_cache(batch.n_pages, 1, 64, 16)
+    x = torch.full((3, 192), 0.5, dtype=torch.float16)
+    x[1, 64 + 5], x[2, 128 + 7], x[0, 128 + 63] = float("inf"), float("-inf"), float("inf")
+    freq, axis = torch.zeros(32, dtype=torch.float64, device=dev()), torch.zeros(32, dtype=torch.int32, device=dev())
+    say("infinite values")
+    rbl.rope_append_kv8(x.to(dev()), cache, batch.cu, batch.kv_lens, batch.table, 3, 1,
+                        torch.ones(3, 1, dtype=torch.int32, device=dev()), freq, axis)
+    torch.cuda.synchronize()
+    i = batch.page(0, 0)
+    for codes, scale, bad in ((cache.k[i, 0, :3], cache.k_scale[i, 0], {(1, 5), (1, 37)}),
+                              (cache.v[i, 0, :, :3].t().contiguous(), cache.v_scale[i, 0], {(2, 7), (0, 63)})):
+        assert scale.item() == 2.0 ** -9                  # 0.5 / 2^-9 = 256, and 512 would exceed 448
+        got = codes.cpu().view(F8).float() * scale.item()
+        nan = {tuple(t) for t in torch.isnan(got).nonzero().tolist()}
+        assert nan and nan <= bad and (got[~torch.isnan(got)] == 0.5).all().item()
+
+
 def test_bad_pages_and_bounds_store_nothing():
     batch = Batch([70, 70, 5, 3], [70, 70, 5, 3], seed=10)
     batch.table_cpu[0, 1] = -1
