@@ -92,8 +92,17 @@ struct NormWeights { float c[16]; };
 // weights of a segment (1 where there are none, 0 past K)
 __device__ __forceinline__ void load_weights(const float *w, int64_t k0, int64_t K, NormWeights &n)
 {
+    if (w && k0 + 16 <= K) {
+        __builtin_memcpy(n.c, w + k0, 64);               // 4-byte aligned
+        return;
+    }
+    const int rem = opaque((int)(K - k0 < 16 ? K - k0 : 16));
 #pragma unroll
-    for (int i = 0; i < 16; i++) n.c[i] = k0 + i < K ? (w ? w[k0 + i] : 1.0f) : 0.0f;
+    for (int i = 0; i < 16; i++) n.c[i] = i < rem ? 1.0f : 0.0f;
+    if (!w) return;
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        if (i < rem) n.c[i] = w[k0 + i];
 }
 
 // sum over the 16 lanes of a group, the same bits in every lane (the DPP exchanges of group16_umax)

@@ -46,7 +46,7 @@ struct RopeArgs {
     int n_axes;
     int Hq, Hkv;
     int visits;          // pages that the longest run of new tokens may touch
-    int tokens;          // NT, a power of two
+    int log_tokens;      // of NT
     int q_chunks, kv_chunks;   // workgroups that share a page's heads (each takes every so-manieth)
     uint32_t q_blocks;
     float eps;
@@ -184,9 +184,9 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
     const int nt = (int)(hi - lo), off0 = (int)(lo - pg * kPage);
     const int64_t row0 = t0 + (lo - first);
 
-    const int NT = a.tokens, HP = TEAMS / NT;              // tokens and heads at a time
+    const int NT = 1 << a.log_tokens, HP = TEAMS >> a.log_tokens;   // tokens and heads at a time
     const int tid = threadIdx.x, c = tid % TEAM, team = tid / TEAM;
-    const int tk = team % NT, slot = team / NT;
+    const int tk = team & (NT - 1), slot = team >> a.log_tokens;
 
     // ---- cosine and sine of this lane's pairs, shared by the workgroup's heads ----
     const float *weight = is_q ? a.q_weight : a.k_weight;
@@ -202,25 +202,41 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
         r0 = fetch16<D, IL>(qkv + ((is_q ? 0 : a.Hq) + h0 + slot) * D, c);
         if (!is_q) r1 = fetch16<D, false>(qkv + (a.Hq + a.Hkv + h0 + slot) * D, c);
     }
-    Turn turn;
-    if (live) {
-        const int32_t *p = a.pos + row * a.ld_pos;
+    // every table entry in flight at once; of the positions all axes' are loaded and one selected,
+    // so that no load waits for another
+    float wa[8], wb[8];
+    double freq[8];
+    uint32_t axis[8];
+    int32_t at[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i++) wa[i] = wb[i] = 1.0f;
+    if (weight) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const int ax = min((uint32_t)a.axis[8 * c + i], (uint32_t)(a.n_axes - 1));
-            const double turns = (double)p[ax] * (a.freq[8 * c + i] * 0.15915494309189533577);   // 1 / (2 pi)
-            const float part = (float)(turns - rint(turns));
-            const float si = __builtin_amdgcn_sinf(part), co = __builtin_amdgcn_cosf(part);
-            float wa = 1.0f, wb = 1.0f;
-            if (weight) {
-                wa = weight[IL ? 16 * c + 2 * i : 8 * c + i];
-                wb = weight[IL ? 16 * c + 2 * i + 1 : D / 2 + 8 * c + i];
-            }
-            turn.ca[i] = wa * co;
-            turn.sa[i] = wa * si;
-            turn.cb[i] = wb * co;
-            turn.sb[i] = wb * si;
+            wa[i] = weight[IL ? 16 * c + 2 * i : 8 * c + i];
+            wb[i] = weight[IL ? 16 * c + 2 * i + 1 : D / 2 + 8 * c + i];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        freq[i] = a.freq[8 * c + i];
+        axis[i] = a.axis[8 * c + i];
+    }
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) at[i] = a.pos[row * a.ld_pos + min(i, a.n_axes - 1)];
+    }
+    Turn turn;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int32_t pos = axis[i] == 0 ? at[0] : axis[i] == 1 ? at[1] : axis[i] == 2 ? at[2] : at[3];   // beyond: the last
+        const double turns = (double)pos * (freq[i] * 0.15915494309189533577);                         // 1 / (2 pi)
+        const float part = (float)(turns - rint(turns));
+        const float si = __builtin_amdgcn_sinf(part), co = __builtin_amdgcn_cosf(part);
+        turn.ca[i] = wa[i] * co;
+        turn.sa[i] = wa[i] * si;
+        turn.cb[i] = wb[i] * co;
+        turn.sb[i] = wb[i] * si;
     }
     if (is_q) {
         if (!live) return;                                 // whole teams, no barrier on this side
@@ -338,17 +354,16 @@ template <int DT, int D>
 static hipError_t launch_rope(RopeArgs a, int64_t B, int64_t max_new, bool interleaved, int cus, hipStream_t st)
 {
     constexpr int TEAMS = 64;
-    int nt = 1;
-    while (nt < max_new && nt < kPage) nt *= 2;
-    a.tokens = nt;
-    const int hp = TEAMS / nt;
+    while ((1 << a.log_tokens) < max_new && (1 << a.log_tokens) < kPage) a.log_tokens++;
+    const int hp = TEAMS >> a.log_tokens;
     a.visits = (int)((max_new + kPage - 2) / kPage + 1);
     // heads per workgroup: a multiple of those it takes at a time, as many as leave four
-    // workgroups for every compute unit (the sines are then shared by more heads), at most 16 steps
+    // workgroups for every compute unit (the sines are then shared by more heads), at most 8
+    // steps (19989 tokens, 56 heads: 318 us with 16, 301 with 8; 8 heads with 4: 50 us, with 2: 58)
     const int64_t pages = B * a.visits;
     auto chunks = [&](int run) { return (a.Hq + run - 1) / run + (a.Hkv + run - 1) / run; };
     int run = hp;
-    while (run < 16 * hp && pages * chunks(2 * run) >= 4 * (int64_t)cus) run *= 2;
+    while (run < 8 * hp && pages * chunks(2 * run) >= 4 * (int64_t)cus) run *= 2;
     a.q_chunks = (a.Hq + run - 1) / run;
     a.kv_chunks = (a.Hkv + run - 1) / run;
     const int64_t blocks = pages * chunks(run);
