@@ -645,9 +645,9 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
 #pragma unroll
         for (int kb = 0; kb < 4; kb++)
 #pragma unroll
-            for (int c = 0; c < C; c++) kr[kb][c] = *reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c);
+            for (int c = 0; c < C; c++) kr[kb][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c));
 #pragma unroll
-        for (int d = 0; d < D / 16; d++) vr[d] = *reinterpret_cast<const u32x4v *>(vp + 16 * d * kPage);
+        for (int d = 0; d < D / 16; d++) vr[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(vp + 16 * d * kPage));
         const float ks = a.k_scale[at], vs = a.v_scale[at];
 
         f32x4 sc[4];
@@ -759,14 +759,17 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
 }
 
 // --------------------------------------------------------------- joining the splits ----
-// One wave per row of the split blocks: the runs that hold keys the row sees, in order.
-template <int DT, int D>
+// W waves per row of the split blocks: the runs that hold keys the row sees, each wave's in order,
+// the waves' sums through LDS.
+template <int DT, int D, int W>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int E = D / 64;
+    __shared__ float part[4][D + 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;
     const int64_t stride = (int64_t)a.tail * rows;       // rows of one split
-    if (id >= stride) return;
+    if (id >= stride) return;                            // whole workgroups where waves share a row
     const Task task = task_of(a, a.whole + (int)(id / rows));
     const Seq s = load_seq(a, task.b);
     const int r = task.block * rows + (int)(id % rows);
@@ -778,15 +781,27 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
     for (int i = lane; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + id].x);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    constexpr int E = D / 64;
     float acc[E] = {}, sum = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < n; i++) {
+#pragma unroll 8
+    for (int i = wave % W; i < n; i += W) {
         const float2 ml = a.part_ml[i * stride + id];
         const float f = __builtin_amdgcn_exp2f(ml.x - top);
         sum = fmaf(ml.y, f, sum);
 #pragma unroll
         for (int e = 0; e < E; e++) acc[e] = fmaf(a.part_o[(i * stride + id) * D + E * lane + e], f, acc[e]);
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; e++) part[wave][E * lane + e] = acc[e];
+        if (lane == 0) part[wave][D] = sum;
+        __syncthreads();
+        if (wave != 0) return;
+#pragma unroll
+        for (int w = 1; w < W; w++) {
+#pragma unroll
+            for (int e = 0; e < E; e++) acc[e] += part[w][E * lane + e];
+            sum += part[w][D];
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *po = a.out + (s.t0 + tok) * a.ld_out + (task.hk * a.G + (r - tok * a.G)) * D + E * lane;
@@ -804,7 +819,7 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     p.splits = p.pages_per_split = p.row_blocks = 1;
     if (T == 0 || B == 0 || max_q == 0 || Hq == 0) return p;
     const int64_t rows = max_q * (Hq / Hkv);
-    p.few = rows <= 2 * kFewRows;
+    p.few = rows <= kFewRows;
     const int per = p.few ? kFewRows : kRowsBlock;
     p.row_blocks = (rows + per - 1) / per;
     const int64_t pages = max_kv > 0 ? (max_kv + kPage - 1) / kPage : 1;
@@ -815,9 +830,19 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     const int64_t base = B * Hkv * p.row_blocks;
     p.whole = base;
     if (p.few) {
-        // eight workgroups a compute unit, of at least a page a wave
-        int64_t n = (8 * (int64_t)cus + base - 1) / base;
-        if (n > pages / 4) n = pages / 4;
+        // Where the blocks fill the device (three workgroups a compute unit), runs short enough to
+        // even out ragged lengths, but of 16 pages: 64 sequences of up to 32768 tokens, 8
+        // key/value heads, 403 us in sixteen workgroups a compute unit, 431 in eight, 412 in 32.
+        // Else enough runs to fill it once, at least 8 while that is within sixteen, of a page a
+        // wave or more: one sequence of 131072 tokens in 96 runs 51 us, in 512 105 us.
+        const int64_t slots = 3 * (int64_t)cus, fine = 16 * (int64_t)cus / base;
+        int64_t n = fine;
+        if (base < slots) {
+            n = (slots + base - 1) / base;
+            if (n < 8) n = fine < 8 ? fine : 8;
+        }
+        const int64_t most = pages / (base >= slots ? 16 : 4);
+        if (n > most) n = most;
         if (n > 1) {
             p.whole = 0;
             p.splits = n;
@@ -863,7 +888,10 @@ static hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, hipStream_t 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.tail == 0) return e;
     const int rows = p.few ? kFewRows : kRowsBlock;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D>), dim3((unsigned)((p.tail * rows + 3) / 4)), dim3(256), 0, st, a, rows);
+    // many runs: four waves a row
+    const int64_t n = p.tail * rows;
+    if (p.splits > 8) hipLaunchKernelGGL((attn_join_kernel<DT, D, 4>), dim3((unsigned)n), dim3(256), 0, st, a, rows);
+    else hipLaunchKernelGGL((attn_join_kernel<DT, D, 1>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, a, rows);
     return hipGetLastError();
 }
 
