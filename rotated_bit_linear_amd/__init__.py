@@ -137,7 +137,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:                             # the current stream's handle, without a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -154,15 +154,20 @@ def _rows_ld(t: torch.Tensor):
     return t.size(0), st[0]
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    """cr_dtype of a tensor (-1, which every call rejects, for types the library does not know)."""
-    return _TORCH_TO_CR.get(t.dtype, -1)
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a row-major 2-D tensor."""
+    st = t.stride()
+    assert len(st) == 2 and st[1] == 1, "expected a row-major 2-D tensor (unit column stride)"
+    return st[0]
 
 
-def _check_vector(name: str, t, n: int, dtype=torch.float32):
-    """An optional contiguous vector argument of at least n elements."""
-    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() < n):
+def _vector(name: str, t, n: int, dtype=torch.float32) -> int | None:
+    """Address of an optional contiguous vector argument of at least n elements."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {n} elements")
+    return t.data_ptr()
 
 
 def padded_k(k: int) -> int:
@@ -209,18 +214,18 @@ def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=
     r = h = None
     ld_r = ld_h = 0
     if residual is not None:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
+        if residual.shape != x.shape or residual.dtype is not x.dtype:
             raise ValueError("residual must have the shape and dtype of x")
-        r, ld_r = residual.data_ptr(), _rows_ld(residual)[1]
+        r, ld_r = residual.data_ptr(), _ld(residual)
     if sum is not None:
-        if sum.shape != x.shape or sum.dtype != x.dtype:
+        if sum.shape != x.shape or sum.dtype is not x.dtype:
             raise ValueError("sum must have the shape and dtype of x")
-        h, ld_h = sum.data_ptr(), _rows_ld(sum)[1]
-    _check_vector("weight", weight, K)
+        h, ld_h = sum.data_ptr(), _ld(sum)
     status = lib().cr_quant_act_rmsnorm(
-        x.data_ptr(), _dtype_code(x), ld_x, r, ld_r, h, ld_h, _ptr(weight), eps, M, K, x_s8.data_ptr(),
-        _rows_ld(x_s8)[1], x_scale.data_ptr(), flags, _stream(stream))
-    _check("cr_quant_act_rmsnorm", status)
+        x.data_ptr(), _TORCH_TO_CR.get(x.dtype, -1), ld_x, r, ld_r, h, ld_h, _vector("weight", weight, K), eps, M, K,
+        x_s8.data_ptr(), _ld(x_s8), x_scale.data_ptr(), flags, _stream(stream))
+    if status:
+        raise CrError("cr_quant_act_rmsnorm", status)
 
 
 def cr_swiglu(h, F, out, stream=None):
@@ -450,43 +455,43 @@ class Kv8Cache:
 
     def _with_table(self, page_table: torch.Tensor) -> _Kv8:
         return _Kv8(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                    self.n_pages, page_table.data_ptr(), page_table.size(1))
+                    self.n_pages, page_table.data_ptr(), page_table.shape[1])
 
 
 def _check_batch(cu_seqlens, kv_lens, page_table):
     B = kv_lens.numel()
-    if cu_seqlens.dtype != torch.int32 or kv_lens.dtype != torch.int32 or cu_seqlens.numel() != B + 1 \
+    i32 = torch.int32
+    if cu_seqlens.dtype is not i32 or kv_lens.dtype is not i32 or cu_seqlens.numel() != B + 1 \
             or not cu_seqlens.is_contiguous() or not kv_lens.is_contiguous():
         raise ValueError("cu_seqlens [B + 1] and kv_lens [B] must be contiguous int32 tensors")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.size(0) != B \
-            or not page_table.is_contiguous():
+    shape = page_table.shape
+    if page_table.dtype is not i32 or len(shape) != 2 or shape[0] != B or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 tensor [B, pages per sequence]")
     return B
 
 
 def cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight, eps, pos, freq, axis, q_out, cache,
                        page_table, flags=0, stream=None):
-    T, ld = _rows_ld(qkv)
     B = _check_batch(cu_seqlens, kv_lens, page_table)
     D, Hkv = cache.D, cache.Hkv
-    if qkv.size(1) != (Hq + 2 * Hkv) * D:
+    ld, width = _ld(qkv), Hq * D
+    T, cols = qkv.shape
+    if cols != width + 2 * Hkv * D:
         raise ValueError(f"qkv must hold {Hq} + 2 * {Hkv} heads of {D} elements a row")
-    if q_out.dtype != qkv.dtype or q_out.shape != (T, Hq * D):
+    if q_out.dtype is not qkv.dtype or q_out.shape != (T, width):
         raise ValueError("q_out must be [T, Hq * D] of qkv's dtype")
-    n_axes = pos.size(-1)
-    n_pos, ld_pos = _rows_ld(pos)
-    if pos.dtype != torch.int32 or n_pos != T:
+    ld_pos = _ld(pos)
+    n_pos, n_axes = pos.shape
+    if pos.dtype is not torch.int32 or n_pos != T:
         raise ValueError("pos must be int32 [T, axes]")
-    _check_vector("q_weight", q_weight, D)
-    _check_vector("k_weight", k_weight, D)
-    _check_vector("freq", freq, D // 2, torch.float64)
-    _check_vector("axis", axis, D // 2, torch.int32)
     status = lib().cr_rope_append_kv8(
-        qkv.data_ptr(), _dtype_code(qkv), ld, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_new, Hq, Hkv, D,
-        _ptr(q_weight), _ptr(k_weight), eps, pos.data_ptr(), max(ld_pos, n_axes), n_axes, freq.data_ptr(),
-        axis.data_ptr(), q_out.data_ptr(), max(_rows_ld(q_out)[1], Hq * D), cache._with_table(page_table), flags,
-        _stream(stream))
-    _check("cr_rope_append_kv8", status)
+        qkv.data_ptr(), _TORCH_TO_CR.get(qkv.dtype, -1), ld, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_new,
+        Hq, Hkv, D, _vector("q_weight", q_weight, D), _vector("k_weight", k_weight, D), eps, pos.data_ptr(),
+        max(ld_pos, n_axes), n_axes, _vector("freq", freq, D // 2, torch.float64),
+        _vector("axis", axis, D // 2, torch.int32), q_out.data_ptr(), max(_ld(q_out), width),
+        cache._with_table(page_table), flags, _stream(stream))
+    if status:
+        raise CrError("cr_rope_append_kv8", status)
 
 
 def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
@@ -495,16 +500,18 @@ def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
 
 def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm_scale, out, workspace, flags=0,
                 stream=None):
-    T, ld_q = _rows_ld(q)
     B = _check_batch(cu_seqlens, kv_lens, page_table)
-    D, width = cache.D, Hq * cache.D
-    if q.size(1) != width or out.shape != q.shape or out.dtype != q.dtype:
+    ld_q, shape, D = _ld(q), q.shape, cache.D
+    T, width = shape
+    if width != Hq * D or out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("q and out must be [T, Hq * D] of one dtype")
     status = lib().cr_attn_kv8(
-        q.data_ptr(), _dtype_code(q), max(ld_q, width), T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_q, max_kv,
-        Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), max(_rows_ld(out)[1], width),
-        _ptr(workspace), 0 if workspace is None else workspace.nbytes, flags, _stream(stream))
-    _check("cr_attn_kv8", status)
+        q.data_ptr(), _TORCH_TO_CR.get(q.dtype, -1), max(ld_q, width), T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(),
+        max_q, max_kv, Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), max(_ld(out), width),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, flags,
+        _stream(stream))
+    if status:
+        raise CrError("cr_attn_kv8", status)
 
 
 # ---------------------------------------------------------------- conveniences ----
@@ -532,10 +539,10 @@ def quant_act_rmsnorm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: 
     residual: updated in place) or to a new tensor; None without a residual."""
     M, K = x.shape
     d = x.device
-    q = torch.empty((M, (K + 255) // 256 * 256), dtype=torch.int8, device=d)
+    q = torch.empty(M, (K + 255) // 256 * 256, dtype=torch.int8, device=d)
     s = torch.empty(M, dtype=torch.float32, device=d)
     if residual is not None and sum is None:
-        n = 16 // x.element_size()
+        n = 16 // x.element_size()                 # rows of 16-byte multiples
         sum = x.new_empty(M, K) if K % n == 0 else x.new_empty(M, (K + n - 1) // n * n)[:, :K]
     cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, q, s, flags)
     return q, s, sum
@@ -695,7 +702,7 @@ def rope_append_kv8(qkv, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_n
     projection; their keys and values go to the cache.  kv_lens counts the new tokens.  `out` may
     be qkv[:, : Hq * D]."""
     if out is None:
-        out = qkv.new_empty(qkv.size(0), Hq * cache.D)
+        out = qkv.new_empty(qkv.shape[0], Hq * cache.D)
     cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight, eps, pos, freq, axis, out, cache,
                        page_table, CR_FLAG_ROPE_INTERLEAVED if interleaved else 0)
     return out
@@ -705,9 +712,9 @@ def attn_kv8(q, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_q: int, ma
              sm_scale: float | None = None, causal: bool = True, out=None, workspace=None):
     """Attention of q [T, Hq * D] over the cached keys and values; sm_scale defaults to 1/sqrt(D)."""
     if out is None:
-        out = q.new_empty(q.size(0), Hq * cache.D)
+        out = q.new_empty(q.shape[0], Hq * cache.D)
     if workspace is None:
-        need = cr_attn_kv8_workspace_bytes(q.size(0), kv_lens.numel(), max_q, max_kv, Hq, cache.Hkv, cache.D)
+        need = cr_attn_kv8_workspace_bytes(q.shape[0], kv_lens.numel(), max_q, max_kv, Hq, cache.Hkv, cache.D)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table,
                 cache.D ** -0.5 if sm_scale is None else sm_scale, out, workspace, CR_FLAG_CAUSAL if causal else 0)
