@@ -11,9 +11,9 @@
 // the contraction may take keys in any order, so V^T is presented in the order in which S^T
 // leaves them.
 // Precision: codes are exact in bf16 and fp16, products accumulate in FP32, maximum and sum
-// are FP32.  P is rounded to fp16 whatever the queries' type (half a step is 2^-12 of p, and
-// 2^-25 below 2^-14; the second product takes the codes as fp16): in bf16 its rounding
-// would double the variance of a bf16 output's error.
+// are FP32.  P is rounded to fp16 whatever the queries' type (half a step is at most 2^-11 of
+// p, and 2^-25 below 2^-14; the second product takes the codes as fp16): in bf16, half a
+// step is 2^-8, and a row that one key dominates would be off by that twice.
 // Scales: a page's key scale joins the factor of the exponent's argument, its value scale
 // the exponent: P holds p * vs / vref, vref the largest value scale so far (the accumulators
 // are rescaled when it grows), so 16-bit P never overflows.  A value scale below 2^-64 vref
@@ -144,6 +144,9 @@ __device__ __forceinline__ int opaque_lane(int v)
 // pins the computation of v to this place (the compiler would sink it out of the products' shadow)
 __device__ __forceinline__ void stay(float &v) { asm volatile("" : "+v"(v)); }
 
+// waits for all of this wave's LDS operations
+__device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // a barrier that waits for this wave's LDS operations but the last `younger` (its operand reads)
 template <int younger>
 __device__ __forceinline__ void barrier_but()
@@ -219,21 +222,21 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 }  // namespace
 
 // ------------------------------------------------------------------ prompts: many rows ----
-// One workgroup: NC blocks of 32 query rows in each of 4 waves over a run of pages.  A page is
+// One workgroup: 32 query rows in each of 4 waves over a run of pages.  A page is
 // read once into registers, widened to 16 bits, and written to one of two LDS tiles in the
 // order in which the matrix operands want it; rows are padded by 16 bytes so that the 16
 // lanes of a read cover all banks.
 // Software pipeline over halves of a page (32 keys): a step issues the score products of the
 // next half, the softmax of this one under them, this half's second products, and under
 // those the widening of half a page to come; one barrier a step.
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kRowsBlock = 32 * kWaves;
 
-template <int DT, int D, int NC>
+template <int DT, int D>
 __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArgs a)
 {
     constexpr int KROW = 2 * D + 16, VROW = 2 * kPage + 16;   // bytes of a widened row of keys, of values
     constexpr int KQ = D / 64, VQ = D / 64;             // 16-byte code loads a thread and tile
-    constexpr int ROWS = 32 * NC * kWaves;
+    constexpr int ROWS = kRowsBlock;
     __shared__ __attribute__((aligned(16))) uint8_t ldsK[2][kPage * KROW];
     __shared__ __attribute__((aligned(16))) uint8_t ldsV[2][D * VROW];
     __shared__ uint32_t nan_keys[3][2];                 // keys of a tile whose values hold NaN codes
@@ -255,19 +258,17 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     const int p1 = task.split < 0 || task.split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
     if (task.split >= 0 && p0 >= p1) return;               // no row of the block looks here
 
-    const bool busy = r0 + wave * NC * 32 < s.rows;     // a wave without rows only stages
-    int lim[NC];
-    u32x4v q[NC][D / 16];
-#pragma unroll
-    for (int n = 0; n < NC; n++) {
+    const bool busy = r0 + wave * 32 < s.rows;     // a wave without rows only stages
+    int lim;
+    u32x4v q[D / 16];
+    {
         // rows past the last repeat it and are not stored
-        const int r = min(r0 + (wave * NC + n) * 32 + col, s.rows - 1);
-        const int i_tok = r / a.G;
-        lim[n] = visible(a, s, i_tok);
+        const int r = min(r0 + wave * 32 + col, s.rows - 1), i_tok = r / a.G;
+        lim = visible(a, s, i_tok);
 #pragma unroll
         for (int k = 0; k < D / 16; k++)
-            q[n][k] = *reinterpret_cast<const u32x4v *>(a.q + (s.t0 + i_tok) * a.ld_q + (hk * a.G + (r - i_tok * a.G)) * D +
-                                                        16 * k + 8 * half);
+            q[k] = *reinterpret_cast<const u32x4v *>(a.q + (s.t0 + i_tok) * a.ld_q + (hk * a.G + (r - i_tok * a.G)) * D +
+                                                     16 * k + 8 * half);
     }
 
     // ---- staging: codes of a page in registers, then widened in LDS ----
@@ -318,17 +319,12 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     };
 
     // ---- the parts of a page ----
-    f32x16 o[NC][D / 32];
-    float m[NC], l[NC], mx[NC], vref = kMinScale;
+    f32x16 o[D / 32];
 #pragma unroll
-    for (int n = 0; n < NC; n++) {
-        m[n] = kLow;
-        l[n] = 0.0f;
+    for (int d = 0; d < D / 32; d++)
 #pragma unroll
-        for (int d = 0; d < D / 32; d++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) o[n][d][e] = 0.0f;
-    }
+        for (int e = 0; e < 16; e++) o[d][e] = 0.0f;
+    float m = kLow, l = 0.0f, mx = 0.0f, vref = kMinScale;
     // operand i of the score products with 32 keys (half kb of a tile), of the second products
     const int lane_k = col * KROW + 16 * half, lane_v = col * VROW + 16 * half;
     auto read_k = [&](int buf, int kb, int i) __attribute__((always_inline)) {
@@ -338,45 +334,36 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         const int j = i / (D / 32), d = i % (D / 32);
         return *reinterpret_cast<const u32x4v *>(ldsV[buf] + lane_v + 32 * d * VROW + 32 * (2 * kb + j));
     };
-    auto mask = [&](f32x16 (&x)[NC], int p, int kb, bool ok) __attribute__((always_inline)) {
+    auto mask = [&](f32x16 &x, int p, int kb, bool ok) __attribute__((always_inline)) {
         const uint32_t bad = nan_keys[p % 3][kb] >> (4 * half);
+        const int left = (ok ? lim - p * kPage : 0) - 32 * kb - 4 * half;
 #pragma unroll
-        for (int n = 0; n < NC; n++) {
-            const int left = (ok ? lim[n] - p * kPage : 0) - 32 * kb - 4 * half;
-#pragma unroll
-            for (int e = 0; e < 16; e++) {
-                const int key = 8 * (e >> 2) + (e & 3);
-                const float y = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : x[n][e];
-                x[n][e] = key < left ? y : -__builtin_inff();
-            }
+        for (int e = 0; e < 16; e++) {
+            const int key = 8 * (e >> 2) + (e & 3);
+            const float y = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : x[e];
+            x[e] = key < left ? y : -__builtin_inff();
         }
     };
-    float top[NC];                                      // largest score of the half page so far
-    auto max_of = [&](const f32x16 (&x)[NC], int e0, int e1) __attribute__((always_inline)) {
+    float top;                                          // largest score of the half page so far
+    auto max_of = [&](const f32x16 &x, int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NC; n++)
-#pragma unroll
-            for (int e = e0; e < e1; e++) top[n] = e == 0 ? x[n][0] : fmaxf(top[n], x[n][e]);
-#pragma unroll
-        for (int n = 0; n < NC; n++) stay(top[n]);
+        for (int e = e0; e < e1; e++) top = e == 0 ? x[0] : fmaxf(top, x[e]);
+        stay(top);
     };
-    auto row_max = [&](float c) __attribute__((always_inline)) {
+    auto rescale = [&](float f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NC; n++) mx[n] = both_halves_max(top[n]) * c;
+        for (int d = 0; d < D / 32; d++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) o[d][e] *= f;
     };
     // the maximum of the scores about to be added: rescales what is there where it grows (rare)
     auto raise = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int n = 0; n < NC; n++)
-            if (__builtin_amdgcn_ballot_w64(mx[n] > m[n] + kSlack) != 0) {
-                const float m1 = fmaxf(m[n], mx[n]), f = __builtin_amdgcn_exp2f(m[n] - m1);
-                m[n] = m1;
-                l[n] *= f;
-#pragma unroll
-                for (int d = 0; d < D / 32; d++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++) o[n][d][e] *= f;
-            }
+        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
+            const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= f;
+            rescale(f);
+        }
     };
     // the value scale of the page about to be added, likewise: its shift of the exponents and
     // weight in the sum
@@ -386,30 +373,22 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         if (vsx > vref) {                               // uniform
             const float f = vref * __builtin_amdgcn_rcpf(vsx);
             vref = vsx;
-#pragma unroll
-            for (int n = 0; n < NC; n++)
-#pragma unroll
-                for (int d = 0; d < D / 32; d++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++) o[n][d][e] *= f;
+            rescale(f);
         }
         shift = __builtin_amdgcn_logf(vsx) - __builtin_amdgcn_logf(vref);
         weight = vref * __builtin_amdgcn_rcpf(vsx);
     };
-    u32x4v pk[NC][2];
-    float sum[NC];
-    auto softmax = [&](const f32x16 (&x)[NC], float c, int e0, int e1) __attribute__((always_inline)) {
+    u32x4v pk[2];
+    float sum;
+    auto softmax = [&](const f32x16 &x, float c, int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < NC; n++)
-#pragma unroll
-            for (int e = e0; e < e1; e += 2) {
-                const float y = __builtin_amdgcn_exp2f(fmaf(x[n][e], c, shift - m[n]));
-                const float z = __builtin_amdgcn_exp2f(fmaf(x[n][e + 1], c, shift - m[n]));
-                sum[n] = e == 0 ? y + z : sum[n] + (y + z);
-                pk[n][e >> 3][(e >> 1) & 3] = Half<1>::pack(y, z);
-            }
-#pragma unroll
-        for (int n = 0; n < NC; n++) stay(sum[n]);
+        for (int e = e0; e < e1; e += 2) {
+            const float y = __builtin_amdgcn_exp2f(fmaf(x[e], c, shift - m));
+            const float z = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c, shift - m));
+            sum = e == 0 ? y + z : sum + (y + z);
+            pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(y, z);
+        }
+        stay(sum);
     };
     // A step: softmax of x (half kb of page p, tile bv of the values) and its second products;
     // scores of the next half into y (half kb ^ 1 of tile bk of the keys); one tile's widening
@@ -418,37 +397,35 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     // read, and as much vector work follows as the product takes.
     constexpr int NQ = D / 16, NV = D / 16, AHEAD = D == 64 ? 3 : 4, RING = D == 64 ? 4 : 8;
     u32x4v f[RING];
-    auto step = [&](int kb, const f32x16 (&x)[NC], f32x16 (&y)[NC], float c, int bk, int bv, int bk1,
+    auto step = [&](int kb, const f32x16 &x, f32x16 &y, float c, int bk, int bv, int bk1,
                     auto widen) __attribute__((always_inline)) {
         if (!busy) {                                    // uniform in the wave
 #pragma unroll
             for (int i = 0; i < NV / 2; i++) widen(i);
+            lds_done();                                 // no operand reads follow that the barrier may leave out
             return;
         }
+        __builtin_amdgcn_s_setprio(1);                  // a wave at its products before one at its scales and barriers
 #pragma unroll
         for (int t = 0; t < NQ + NV; t++) {
             const int u = t + AHEAD;
             f[u % RING] = u < NQ ? read_k(bk, kb ^ 1, u) : u < NQ + NV ? read_v(bv, kb, u - NQ) : read_k(bk1, kb, u - NQ - NV);
             if (t < NQ) {
+                if (t == 0)
 #pragma unroll
-                for (int n = 0; n < NC; n++) {
-                    if (t == 0)
-#pragma unroll
-                        for (int e = 0; e < 16; e++) y[n][e] = 0.0f;
-                    y[n] = Half<DT>::mfma32(f[t % RING], q[n][t], y[n]);
-                }
+                    for (int e = 0; e < 16; e++) y[e] = 0.0f;
+                y = Half<DT>::mfma32(f[t % RING], q[t], y);
                 softmax(x, c, t * (16 / NQ), (t + 1) * (16 / NQ));
             } else {
                 const int i = t - NQ;
-#pragma unroll
-                for (int n = 0; n < NC; n++) o[n][i % (D / 32)] = Half<1>::mfma32(f[t % RING], pk[n][i / (D / 32)], o[n][i % (D / 32)]);
+                o[i % (D / 32)] = Half<1>::mfma32(f[t % RING], pk[i / (D / 32)], o[i % (D / 32)]);
                 if (i < NV / 2) widen(i);
                 else max_of(y, (i - NV / 2) * (32 / NV), (i - NV / 2 + 1) * (32 / NV));
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int n = 0; n < NC; n++) l[n] = fmaf(sum[n], weight, l[n]);
+        __builtin_amdgcn_s_setprio(0);
+        l = fmaf(sum, weight, l);
     };
 
     if (tid < 6) (&nan_keys[0][0])[tid] = 0;
@@ -464,7 +441,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         int32_t id3 = table[min(p0 + 3, pl)];
         float c = score_factor(a.factor, a.k_scale[at]), vs = a.v_scale[at];
         float ks1 = a.k_scale[at1], vs1 = a.v_scale[at1];
-        f32x16 sa[NC], sb[NC];
+        f32x16 sa, sb;
         {
             u32x4v k0[KQ], v0[VQ], k1[KQ];              // all in flight together
             load_k(at, k0);
@@ -482,15 +459,12 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         load_k(at2, kr);
         __syncthreads();
 #pragma unroll
-        for (int n = 0; n < NC; n++) {
+        for (int e = 0; e < 16; e++) sa[e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; e++) sa[n][e] = 0.0f;
-#pragma unroll
-            for (int t = 0; t < NQ; t++) sa[n] = Half<DT>::mfma32(read_k(0, 0, t), q[n][t], sa[n]);
-        }
+        for (int t = 0; t < NQ; t++) sa = Half<DT>::mfma32(read_k(0, 0, t), q[t], sa);
         if (masked(p0, ok)) mask(sa, p0, 0, ok);
         max_of(sa, 0, 16);
-        row_max(c);
+        mx = both_halves_max(top) * c;
 #pragma unroll
         for (int t = 0; t < AHEAD; t++) f[t] = read_k(0, 1, t);
         for (int p = p0; p < pl; p++) {
@@ -500,7 +474,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             raise();
             if (masked(p + 1, ok1)) {
                 clean_v(vr, p + 1);
-                __builtin_amdgcn_s_waitcnt(0xc07f);     // lgkmcnt(0): its notes are written
+                lds_done();                             // its notes are written
             }
             barrier_but<AHEAD>();                       // values p are staged; values p - 1 are read
             if (tid < 2) nan_keys[(p + 2) % 3][tid] = 0;       // read in page p - 1, written after the next barrier
@@ -510,7 +484,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
                 mask(sb, p, 1, ok);
                 max_of(sb, 0, 16);
             }
-            row_max(c);
+            mx = both_halves_max(top) * c;
             raise();
             barrier_but<AHEAD>();                       // keys p + 1 are staged; keys p are read
             // ---- keys 32..63; the scores of keys 0..31 of page p + 1; keys p + 2 staged ----
@@ -522,7 +496,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
                 mask(sa, p + 1, 0, ok);
                 max_of(sa, 0, 16);
             }
-            row_max(c);
+            mx = both_halves_max(top) * c;
             ks1 = a.k_scale[at2];
             vs1 = a.v_scale[at2];
             ok1 = ok2;
@@ -540,47 +514,40 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             mask(sb, pl, 1, ok);
             max_of(sb, 0, 16);
         }
-        row_max(c);
+        mx = both_halves_max(top) * c;
         raise();
         softmax(sb, c, 0, 16);
-#pragma unroll
-        for (int n = 0; n < NC; n++) l[n] = fmaf(sum[n], weight, l[n]);
+        l = fmaf(sum, weight, l);
 #pragma unroll
         for (int i = 0; i < NV; i++)
-#pragma unroll
-            for (int n = 0; n < NC; n++)
-                o[n][i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[n][i / (D / 32)], o[n][i % (D / 32)]);
+            o[i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[i / (D / 32)], o[i % (D / 32)]);
     }
 
-    // ---- the lane's rows (found again rather than kept): dims 32 d + 8 g + 4 half + 0..3 ----
-#pragma unroll
-    for (int n = 0; n < NC; n++) {
-        const float total = l[n] + __shfl_xor(l[n], 32);
-        const int r = r0 + opaque_lane((wave * NC + n) * 32 + col);
-        if (r >= s.rows) continue;
-        if (task.split >= 0) {
-            const int64_t at = (int64_t)task.part * ROWS + (r - r0);
-            float *po = a.part_o + at * D;
-#pragma unroll
-            for (int d = 0; d < D / 32; d++)
-#pragma unroll
-                for (int g = 0; g < 4; g++)
-                    *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
-                        f32x4{o[n][d][4 * g] * vref, o[n][d][4 * g + 1] * vref, o[n][d][4 * g + 2] * vref,
-                              o[n][d][4 * g + 3] * vref};
-            if (half == 0) a.part_ml[at] = float2{m[n], total};
-            continue;
-        }
-        const float inv = total == 0.0f ? 0.0f : vref / total;
-        uint16_t *po = a.out + (s.t0 + r / a.G) * a.ld_out + (hk * a.G + r % a.G) * D;
+    // ---- the lane's row (found again rather than kept): dims 32 d + 8 g + 4 half + 0..3 ----
+    const float total = l + __shfl_xor(l, 32);
+    const int r = r0 + opaque_lane(wave * 32 + col);
+    if (r >= s.rows) return;
+    if (task.split >= 0) {
+        const int64_t at = (int64_t)task.part * ROWS + (r - r0);
+        float *po = a.part_o + at * D;
 #pragma unroll
         for (int d = 0; d < D / 32; d++)
 #pragma unroll
             for (int g = 0; g < 4; g++)
-                *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
-                    u32x2v{Half<DT>::pack(o[n][d][4 * g] * inv, o[n][d][4 * g + 1] * inv),
-                           Half<DT>::pack(o[n][d][4 * g + 2] * inv, o[n][d][4 * g + 3] * inv)};
+                *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
+                    f32x4{o[d][4 * g] * vref, o[d][4 * g + 1] * vref, o[d][4 * g + 2] * vref, o[d][4 * g + 3] * vref};
+        if (half == 0) a.part_ml[at] = float2{m, total};
+        return;
     }
+    const float inv = total == 0.0f ? 0.0f : vref / total;
+    uint16_t *po = a.out + (s.t0 + r / a.G) * a.ld_out + (hk * a.G + r % a.G) * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+            *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
+                u32x2v{Half<DT>::pack(o[d][4 * g] * inv, o[d][4 * g + 1] * inv),
+                       Half<DT>::pack(o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv)};
 }
 
 // ------------------------------------------------------------- single tokens: few rows ----
@@ -811,8 +778,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 
 // ----------------------------------------------------------------------- launching ----
 
-constexpr int kRowBlocks = 1, kRowsBlock = 32 * kWaves * kRowBlocks;
-
 AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int Hq, int Hkv, int D, int cus)
 {
     AttnPlan p{};
@@ -884,7 +849,7 @@ static hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, hipStream_t 
     const int64_t blocks = p.whole + p.tail * p.splits;
     if (blocks > kMostBlocks) return hipErrorInvalidValue;
     if (p.few) hipLaunchKernelGGL((attn_few_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((attn_rows_kernel<DT, D, kRowBlocks>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((attn_rows_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.tail == 0) return e;
     const int rows = p.few ? kFewRows : kRowsBlock;
