@@ -41,14 +41,24 @@ struct NormArgs {
     double eps;
 };
 
-// fetch_seg, with the elements of a segment across K read from clamped places, all in flight
-// at once, where fetch_seg's predicated loads wait for one another (777 rows of 4111 fp16:
-// 16.2 us with those)
-template <int DT, bool kKeep = false>
+// elements [k0, k0 + 16) of a row, zeros past K.  Ordinary loads: a segment is two or four
+// 16-byte loads, each of which touches every cache line of the wave's run, and non-temporal
+// ones fetch lines again that are still wanted (19989 x 5376 bf16 with a residual 157 against
+// 141 us, 4096 x 14336 fp32 76 against 50 us).  The elements of a segment across K are read
+// from clamped places, all in flight at once (777 rows of 4111 fp16 with predicated loads,
+// which wait for one another: 16.2 against 11.6 us).
+template <int DT>
 __device__ __forceinline__ void fetch_stream(const typename Elem<DT>::T *row, int64_t k0, int64_t K, RawSeg<DT> &r)
 {
-    if (k0 + 16 <= K || k0 >= K) {
-        fetch_seg<DT, kKeep>(row, k0, K, true, r);
+    constexpr int NW = DT == 2 ? 4 : 2;
+    if (k0 + 16 <= K) {
+#pragma unroll
+        for (int c = 0; c < NW; c++) r.w[c] = *(reinterpret_cast<const u32x4 *>(row + k0) + c);
+        return;
+    }
+    if (k0 >= K) {
+#pragma unroll
+        for (int c = 0; c < NW; c++) r.w[c] = u32x4{0u, 0u, 0u, 0u};
         return;
     }
     const int rem = opaque((int)(K - k0));                   // 1 .. 15
@@ -171,6 +181,14 @@ __device__ __forceinline__ void weigh(const RawSeg<DT> &h, const NormWeights &w,
     }
 }
 
+// computes v and ss here, so that what they came from is no longer needed
+__device__ __forceinline__ void pin(float (&v)[16], double &ss)
+{
+#pragma unroll
+    for (int i = 0; i < 16; i++) asm volatile("" : "+v"(v[i]));
+    asm volatile("" : "+v"(ss));
+}
+
 // LDS of a workgroup of G groups: G transpose tiles, then two sets (for alternate rows) of G
 // sums and G maxima
 __host__ __device__ constexpr size_t norm_lds_bytes(int groups)
@@ -234,6 +252,11 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs<DT> a, int64_t
     int64_t base = (int64_t)blockIdx.x * rpw;
     fetch(base + slot);
     int parity = 0;
+    // codes are stored after the next row's arrival: a wait for its loads would also wait for
+    // stores issued after them
+    bool pending = false;
+    int8_t *dst = out;
+    u32x4 codes = {};
     for (; base < n_rows; base += step) {
         const int64_t row = base + slot;
         const bool live = active && row < n_rows;
@@ -244,6 +267,8 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs<DT> a, int64_t
             if (live && a.sum) store_seg<DT>(a.sum + row * a.ld_sum, k0, a.K, x);
         }
         weigh<DT>(x, w, v, ss);
+        pin(v, ss);                                  // x is free: the next row lands in the same registers
+        if (pending) __builtin_nontemporal_store(codes, reinterpret_cast<u32x4 *>(dst));
         fetch(row + step);
         hadamard256(v, tile, t, natural != 0);
 #pragma unroll
@@ -252,14 +277,17 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs<DT> a, int64_t
         red.put(grp, t, zmax, ss);
         __syncthreads();
         parity ^= 1;
+        pending = live;
         if (!live) continue;                         // whole 16-lane groups: the DPP steps stay inside active rows
         const RowQuant rq = row_quant<8>(red.row_max(slot * nb, nb, t));
-        store_codes<8>(v, rq, out + row * ld_out, b, t);
+        dst = out + row * ld_out + 16 * (16 * (int64_t)b + t);
+        store_codes(v, rq, reinterpret_cast<int8_t *>(&codes));
         if (b == 0) {
             const double s = red.row_sum(slot * nb, nb, t);
             if (t == 0) scale[row] = norm_scale(rq, s, a.K, a.eps);
         }
     }
+    if (pending) __builtin_nontemporal_store(codes, reinterpret_cast<u32x4 *>(dst));
 }
 
 // Rows streamed twice: pass 1 forms h (and writes it), its squares and the rotated maximum;
@@ -282,9 +310,9 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
         for (int s = 0; s < slices; s++) {
             const int64_t k0 = ((int64_t)(s * G + grp) * 16 + t) * 16;
             RawSeg<DT> x, r;
-            fetch_stream<DT, true>(a.x + row * a.ld_x, k0, a.K, x);
+            fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, x);
             if constexpr (kRes) {
-                fetch_stream<DT, true>(a.r + row * a.ld_r, k0, a.K, r);
+                fetch_stream<DT>(a.r + row * a.ld_r, k0, a.K, r);
                 add_segment<DT>(x, r);
                 if (a.sum) store_seg<DT>(a.sum + row * a.ld_sum, k0, a.K, x);
             }
@@ -304,7 +332,7 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
             const int64_t k0 = ((int64_t)b * 16 + t) * 16;
             RawSeg<DT> x, r;
             if (kRes && a.sum) {
-                fetch_stream<DT, true>(a.sum + row * a.ld_sum, k0, a.K, x);   // this thread's own stores
+                fetch_stream<DT>(a.sum + row * a.ld_sum, k0, a.K, x);   // this thread's own stores
             } else {
                 fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, x);
                 if constexpr (kRes) {
