@@ -559,7 +559,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
 // steps.  Likewise each 16-byte load of K covers two steps of the contraction over D.
 // The four waves of a workgroup take the pages of its run in turn and join through LDS; runs
 // of one row are joined by attn_join_kernel.
-// Bound by the cache's bytes: the waves keep a whole page each in flight.
+// Bound by the cache's bytes: the waves keep a whole page each in flight.  Values are read once
+// by whole cache lines, past the caches; a load of K takes halves of lines (D = 128), whose
+// other halves non-temporal loads would fetch again: 384 us, with both so 405, with neither
+// 413 (64 sequences of up to 32768 tokens, 8 key/value heads: 5.9 TB/s).
 constexpr int kFewRows = 16;
 
 template <int DT, int D>
@@ -612,7 +615,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
 #pragma unroll
         for (int kb = 0; kb < 4; kb++)
 #pragma unroll
-            for (int c = 0; c < C; c++) kr[kb][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c));
+            for (int c = 0; c < C; c++) kr[kb][c] = *reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c);
 #pragma unroll
         for (int d = 0; d < D / 16; d++) vr[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(vp + 16 * d * kPage));
         const float ks = a.k_scale[at], vs = a.v_scale[at];
@@ -797,7 +800,7 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     if (p.few) {
         // Where the blocks fill the device (three workgroups a compute unit), runs short enough to
         // even out ragged lengths, but of 16 pages: 64 sequences of up to 32768 tokens, 8
-        // key/value heads, 403 us in sixteen workgroups a compute unit, 431 in eight, 412 in 32.
+        // key/value heads, 384 us in sixteen workgroups a compute unit (403, 431 in eight and 412 in 32 when measured).
         // Else enough runs to fill it once, at least 8 while that is within sixteen, of a page a
         // wave or more: one sequence of 131072 tokens in 96 runs 51 us, in 512 105 us.
         const int64_t slots = 3 * (int64_t)cus, fine = 16 * (int64_t)cus / base;
