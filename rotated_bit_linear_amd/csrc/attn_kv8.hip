@@ -168,6 +168,10 @@ __device__ __forceinline__ u32x4v load_codes(const uint8_t *base, uint32_t off)
     return *(global_u32x4)(p + off);
 }
 
+// what a kernel only reads, at uniform addresses: scalar loads, whatever it stores elsewhere
+typedef const __attribute__((address_space(4))) int32_t *scalar_i32;
+typedef const __attribute__((address_space(4))) float *scalar_f32;
+
 constexpr float kLow = -1e30f;    // running maximum before the first key
 constexpr float kSlack = 8.0f;    // log2: how far scores may exceed the running maximum
 
@@ -559,14 +563,17 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
 // steps.  Likewise each 16-byte load of K covers two steps of the contraction over D.
 // The four waves of a workgroup take the pages of its run in turn and join through LDS; runs
 // of one row are joined by attn_join_kernel.
-// Bound by the cache's bytes: the waves keep a whole page each in flight.  Values are read once
-// by whole cache lines, past the caches; a load of K takes halves of lines (D = 128), whose
-// other halves non-temporal loads would fetch again: 384 us, with both so 405, with neither
-// 413 (64 sequences of up to 32768 tokens, 8 key/value heads: 5.9 TB/s).
+// Bound by the cache's bytes: twelve waves a compute unit keep a whole page each in flight, the
+// page after it asked for by an id that is there already.  Values are read once by whole cache
+// lines, past the caches; a load of K takes halves of lines (D = 128), whose other halves
+// non-temporal loads would fetch again: 384 us, with both so 405, with neither 413.
+// Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32768 tokens 660 us (6.5 TB/s),
+// of up to 32768 tokens 382 us (6.0); one of 131072 49 us (5.4), of 4097 12 us with its join
+// (8 and 4, both a launch and four dependent loads long).
 constexpr int kFewRows = 16;
 
 template <int DT, int D>
-__global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
+__global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
 {
     constexpr int C = D / 64;                            // 64-byte column runs of a key
     __shared__ float lo[4][kFewRows][D + 4];
@@ -574,19 +581,45 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
 
     const Task task = task_of(a, blockIdx.x);
     const int b = task.b, hk = task.hk;
-    const Seq s = load_seq(a, b);
-    const int r0 = task.block * kFewRows;
-    if (r0 >= s.rows) return;
-
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 15, quarter = lane >> 4;
+    const int p0 = task.split < 0 ? 0 : (int)(task.split * a.pages_per_split);
+
+    // ---- a page's codes and scales ----
+    // the table's entry for page p, or for its last one (never used: no page lies past the table)
+    const scalar_i32 table = (scalar_i32)(a.batch.table + (int64_t)b * a.batch.ld_table);
+    auto entry = [&](int64_t p) __attribute__((always_inline)) { return table[min(p, a.batch.ld_table - 1)]; };
+    auto there = [&](int32_t id) __attribute__((always_inline)) { return id >= 0 && id < a.batch.n_pages; };
+    const int krow = 16 * (col >> 2) + (col & 3);        // + 4 kb
+    u32x4v kr[4][C], vr[D / 16];
+    float ks, vs;
+    auto load_page = [&](int32_t id) __attribute__((always_inline)) {
+        const int64_t at = (int64_t)(there(id) ? id : 0) * a.Hkv + hk;   // page 0 stands in where there is none
+        const uint8_t *kp = a.k + at * (kPage * D) + krow * D + 16 * quarter;
+        const uint8_t *vp = a.v + at * (kPage * D) + col * kPage + 16 * quarter;
+#pragma unroll
+        for (int kb = 0; kb < 4; kb++)
+#pragma unroll
+            for (int c = 0; c < C; c++) kr[kb][c] = *reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c);
+#pragma unroll
+        for (int d = 0; d < D / 16; d++) vr[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(vp + 16 * d * kPage));
+        ks = ((scalar_f32)a.k_scale)[at];
+        vs = ((scalar_f32)a.v_scale)[at];
+    };
+    // the first page is on its way before the lengths are looked at: inside the cache, whatever
+    // the table's unused places hold
+    int32_t id = entry((int64_t)p0 + wave), id1 = entry((int64_t)p0 + wave + 4);
+    const Seq s = load_seq(a, b);
+    load_page(id);
+    asm volatile("" ::: "memory");                       // not moved behind the next branch
+    const int r0 = task.block * kFewRows;
+    if (r0 >= s.rows) return;
     const int r = min(r0 + col, s.rows - 1);             // rows past the last repeat it and are not stored
     const int i_tok = r / a.G, head = hk * a.G + (r - i_tok * a.G);
     const int last = min(r0 + kFewRows, s.rows) - 1;
     const int lim = visible(a, s, i_tok);
     const int lim_all = visible(a, s, r0 / a.G);
     const int pages = (visible(a, s, last / a.G) + kPage - 1) / kPage;
-    const int p0 = task.split < 0 ? 0 : (int)(task.split * a.pages_per_split);
     const int p1 = task.split < 0 || task.split + 1 == a.splits ? pages : (int)min((int64_t)pages, p0 + a.pages_per_split);
     if (task.split >= 0 && p0 >= p1) return;
 
@@ -604,92 +637,83 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnArgs a)
     for (int d = 0; d < D / 16; d++) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLow, l = 0.0f, vref = kMinScale;
 
-    const int krow = 16 * (col >> 2) + (col & 3);        // + 4 kb
     for (int p = p0 + wave; p < p1; p += 4) {
-        const int64_t id = batch_page(a.batch, b, p);
-        if (id < 0) continue;                            // no such page (wave-uniform)
-        const int64_t at = id * a.Hkv + hk;
-        const uint8_t *kp = a.k + at * (kPage * D) + krow * D + 16 * quarter;
-        const uint8_t *vp = a.v + at * (kPage * D) + col * kPage + 16 * quarter;
-        u32x4v kr[4][C], vr[D / 16];
+        if (there(id)) {                                 // uniform in the wave
+            f32x4 sc[4];
 #pragma unroll
-        for (int kb = 0; kb < 4; kb++)
+            for (int kb = 0; kb < 4; kb++) {
+                sc[kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < C; c++) kr[kb][c] = *reinterpret_cast<const u32x4v *>(kp + 4 * kb * D + 64 * c);
+                for (int c = 0; c < C; c++) {
+                    sc[kb] = Half<DT>::mfma16(widen8<DT>(kr[kb][c][0], kr[kb][c][1]), q[c][0], sc[kb]);
+                    sc[kb] = Half<DT>::mfma16(widen8<DT>(kr[kb][c][2], kr[kb][c][3]), q[c][1], sc[kb]);
+                }
+            }
+            if ((p + 1) * kPage > lim_all) {                 // some row does not see all of the page
+                uint32_t bad = 0;                            // this lane's 16 keys whose values hold NaN codes
+                const int inside = s.kv - p * kPage - 16 * quarter;
 #pragma unroll
-        for (int d = 0; d < D / 16; d++) vr[d] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(vp + 16 * d * kPage));
-        const float ks = a.k_scale[at], vs = a.v_scale[at];
-
-        f32x4 sc[4];
+                for (int d = 0; d < D / 16; d++)
 #pragma unroll
-        for (int kb = 0; kb < 4; kb++) {
-            sc[kb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int w = 0; w < 4; w++) {
+                        uint32_t x = vr[d][w] & below_bytes(inside - 4 * w);
+                        const uint32_t n = nan_bytes(x);
+                        bad |= gather_bits(n) << (4 * w);
+                        vr[d][w] = x & ~spread_bytes(n);
+                    }
 #pragma unroll
-            for (int c = 0; c < C; c++) {
-                sc[kb] = Half<DT>::mfma16(widen8<DT>(kr[kb][c][0], kr[kb][c][1]), q[c][0], sc[kb]);
-                sc[kb] = Half<DT>::mfma16(widen8<DT>(kr[kb][c][2], kr[kb][c][3]), q[c][1], sc[kb]);
+                for (int x = 1; x < 16; x <<= 1) bad |= __shfl_xor(bad, x);   // over the dims of the other lanes
+                const int left = lim - p * kPage - 16 * quarter;
+#pragma unroll
+                for (int kb = 0; kb < 4; kb++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int key = 4 * kb + e;
+                        const float x = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : sc[kb][e];
+                        sc[kb][e] = key < left ? x : -__builtin_inff();
+                    }
+            }
+            const float c = score_factor(a.factor, ks);
+            float mx = sc[0][0];
+#pragma unroll
+            for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[e >> 2][e & 3]);
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
+            if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
+                const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
+                m = m1;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < D / 16; d++) o[d] *= f;
+            }
+            const float vsx = fmaxf(fmaxf(vs, kMinScale), vref * 0x1p-64f);
+            if (vsx > vref) {                                // uniform
+                const float f = vref / vsx;
+                vref = vsx;
+#pragma unroll
+                for (int d = 0; d < D / 16; d++) o[d] *= f;
+            }
+            const float shift = __builtin_amdgcn_logf(vsx / vref) - m;
+            float sum = 0.0f;
+            u32x4v pk[2];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], c, shift));
+                const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][(e & 3) + 1], c, shift));
+                sum += x + y;
+                pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(x, y);
+            }
+            l = fmaf(sum, vref / vsx, l);
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) {
+                o[d] = Half<1>::mfma16(widen8<1>(vr[d][0], vr[d][1]), pk[0], o[d]);
+                o[d] = Half<1>::mfma16(widen8<1>(vr[d][2], vr[d][3]), pk[1], o[d]);
             }
         }
-        if ((p + 1) * kPage > lim_all) {                 // some row does not see all of the page
-            uint32_t bad = 0;                            // this lane's 16 keys whose values hold NaN codes
-            const int inside = s.kv - p * kPage - 16 * quarter;
-#pragma unroll
-            for (int d = 0; d < D / 16; d++)
-#pragma unroll
-                for (int w = 0; w < 4; w++) {
-                    uint32_t x = vr[d][w] & below_bytes(inside - 4 * w);
-                    const uint32_t n = nan_bytes(x);
-                    bad |= gather_bits(n) << (4 * w);
-                    vr[d][w] = x & ~spread_bytes(n);
-                }
-#pragma unroll
-            for (int x = 1; x < 16; x <<= 1) bad |= __shfl_xor(bad, x);   // over the dims of the other lanes
-            const int left = lim - p * kPage - 16 * quarter;
-#pragma unroll
-            for (int kb = 0; kb < 4; kb++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int key = 4 * kb + e;
-                    const float x = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : sc[kb][e];
-                    sc[kb][e] = key < left ? x : -__builtin_inff();
-                }
-        }
-        const float c = score_factor(a.factor, ks);
-        float mx = sc[0][0];
-#pragma unroll
-        for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[e >> 2][e & 3]);
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
-        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
-            const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
-            m = m1;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < D / 16; d++) o[d] *= f;
-        }
-        const float vsx = fmaxf(fmaxf(vs, kMinScale), vref * 0x1p-64f);
-        if (vsx > vref) {                                // uniform
-            const float f = vref / vsx;
-            vref = vsx;
-#pragma unroll
-            for (int d = 0; d < D / 16; d++) o[d] *= f;
-        }
-        const float shift = __builtin_amdgcn_logf(vsx / vref) - m;
-        float sum = 0.0f;
-        u32x4v pk[2];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const float x = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][e & 3], c, shift));
-            const float y = __builtin_amdgcn_exp2f(fmaf(sc[e >> 2][(e & 3) + 1], c, shift));
-            sum += x + y;
-            pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(x, y);
-        }
-        l = fmaf(sum, vref / vsx, l);
-#pragma unroll
-        for (int d = 0; d < D / 16; d++) {
-            o[d] = Half<1>::mfma16(widen8<1>(vr[d][0], vr[d][1]), pk[0], o[d]);
-            o[d] = Half<1>::mfma16(widen8<1>(vr[d][2], vr[d][3]), pk[1], o[d]);
-        }
+        if (p + 4 >= p1) break;
+        id = id1;
+        load_page(id);
+        id1 = entry((int64_t)p + 8);                     // a page ahead of its use
     }
 
     // ---- join the waves: row `col`, dims 16 d + 4 quarter .. ----
@@ -800,9 +824,9 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     if (p.few) {
         // Where the blocks fill the device (three workgroups a compute unit), runs short enough to
         // even out ragged lengths, but of 16 pages: 64 sequences of up to 32768 tokens, 8
-        // key/value heads, 384 us in sixteen workgroups a compute unit (403, 431 in eight and 412 in 32 when measured).
+        // key/value heads, 403 us in sixteen workgroups a compute unit, 431 in eight, 412 in 32 (before later steps).
         // Else enough runs to fill it once, at least 8 while that is within sixteen, of a page a
-        // wave or more: one sequence of 131072 tokens in 96 runs 51 us, in 512 105 us.
+        // wave or more: one sequence of 131072 tokens in 96 runs 51 us, in 512 105 us (before later steps).
         const int64_t slots = 3 * (int64_t)cus, fine = 16 * (int64_t)cus / base;
         int64_t n = fine;
         if (base < slots) {
