@@ -13,11 +13,15 @@
 // large rows (|h| above 1.8e19) overflow nor small ones vanish, and the sum's order changes
 // x_scale by at most an ulp.  One FP64 FMA an element is hidden under the loads.
 //
-// Bound by HBM: x, r and h in two (four) bytes and one byte of code an element.  Work split:
-// a 16-lane group per 256-column block as in row_prep.hpp, whole rows in registers up to 64
-// blocks (K_pad 16384; two blocks a group spill beside the second operand and the weights),
-// several short rows a workgroup, the next rows requested while this one is rotated; longer
-// rows are streamed twice.
+// Bound by HBM: x, r and h in two (four) bytes and one byte of code an element; without a
+// residual, 16-bit rows come as near to the vector units' rate (27 operations an element).
+// Work split: a 16-lane group per 256-column block as in row_prep.hpp, whole rows in registers
+// up to 64 blocks (K_pad 16384; two blocks a group spill beside the second operand and the
+// weights), several short rows a workgroup, the next rows requested while this one is rotated;
+// longer rows are streamed twice.
+// Measured: 19989 x 5376 bf16 with a residual 136 us (5.5 TB/s, a 1 GiB copy runs at 5.1), without
+// 62 (5.2); 4096 x 14336 fp32 43 (6.9, partly from the last-level cache; 47 to 50 on rows not
+// there); 21841 x 5377 bf16 173 (4.8); 4096 x 20000 bf16, streamed twice, 175 (3.3); one row 4.3.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -41,24 +45,28 @@ struct NormArgs {
     double eps;
 };
 
-// elements [k0, k0 + 16) of a row, zeros past K.  Ordinary loads: a segment is two or four
-// 16-byte loads, each of which touches every cache line of the wave's run, and non-temporal
-// ones fetch lines again that are still wanted (19989 x 5376 bf16 with a residual 157 against
-// 141 us, 4096 x 14336 fp32 76 against 50 us).  The elements of a segment across K are read
-// from clamped places, all in flight at once (777 rows of 4111 fp16 with predicated loads,
-// which wait for one another: 16.2 against 11.6 us).
+// Elements [k0, k0 + 16) of a row.  Past K: zeros in whole 16-byte chunks; what a chunk holds
+// beyond K is cut by cut_segment once the loads have arrived.  Such a chunk may be read where
+// another row follows (a row's stride covers it, `more`); the last row's elements are read one
+// by one, from clamped places, all in flight at once.
+// Ordinary loads: a segment is two or four 16-byte loads, each of which touches every cache
+// line of the wave's run, and non-temporal ones fetch lines again that are still wanted
+// (19989 x 5376 bf16 with a residual 157 against 141 us, 4096 x 14336 fp32 76 against 50 us).
 template <int DT>
-__device__ __forceinline__ void fetch_stream(const typename Elem<DT>::T *row, int64_t k0, int64_t K, RawSeg<DT> &r)
+__device__ __forceinline__ void fetch_stream(const typename Elem<DT>::T *row, int64_t k0, int64_t K, bool more, RawSeg<DT> &r)
 {
-    constexpr int NW = DT == 2 ? 4 : 2;
+    constexpr int NW = DT == 2 ? 4 : 2;                      // 16-byte chunks
     if (k0 + 16 <= K) {
 #pragma unroll
         for (int c = 0; c < NW; c++) r.w[c] = *(reinterpret_cast<const u32x4 *>(row + k0) + c);
         return;
     }
-    if (k0 >= K) {
+    if (k0 >= K || more) {
 #pragma unroll
-        for (int c = 0; c < NW; c++) r.w[c] = u32x4{0u, 0u, 0u, 0u};
+        for (int c = 0; c < NW; c++) {
+            if (k0 + 16 / NW * c < K) r.w[c] = *(reinterpret_cast<const u32x4 *>(row + k0) + c);
+            else r.w[c] = u32x4{0u, 0u, 0u, 0u};
+        }
         return;
     }
     const int rem = opaque((int)(K - k0));                   // 1 .. 15
@@ -69,14 +77,27 @@ __device__ __forceinline__ void fetch_stream(const typename Elem<DT>::T *row, in
         if constexpr (DT == 2) e[i] = __float_as_uint(*p);
         else e[i] = *p;
     }
-#pragma unroll
-    for (int i = 0; i < 16; i++) e[i] = i < rem ? e[i] : 0u;
     if constexpr (DT == 2) {
 #pragma unroll
         for (int i = 0; i < 16; i++) r.w[i >> 2][i & 3] = e[i];
     } else {
 #pragma unroll
         for (int i = 0; i < 16; i += 2) r.w[i >> 3][(i >> 1) & 3] = e[i] | (e[i + 1] << 16);
+    }
+}
+
+// zeros past K
+template <int DT>
+__device__ __forceinline__ void cut_segment(int64_t k0, int64_t K, RawSeg<DT> &r)
+{
+    if (k0 + 16 <= K || k0 >= K) return;
+    const int rem = (int)(K - k0);                           // 1 .. 15
+    if constexpr (DT == 2) {
+#pragma unroll
+        for (int i = 0; i < 16; i++) r.w[i >> 2][i & 3] = i < rem ? r.w[i >> 2][i & 3] : 0u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) r.w[i >> 2][i & 3] &= 2 * i + 1 < rem ? 0xffffffffu : 2 * i < rem ? 0xffffu : 0u;
     }
 }
 
@@ -106,29 +127,47 @@ __device__ __forceinline__ void add_segment(RawSeg<DT> &r0, const RawSeg<DT> &r1
     }
 }
 
-// a segment's raw bytes to row + k0: 16-byte stores below K, element stores across K
+// a segment's raw bytes to row + k0: 16-byte stores below K, the chunk across K in 8, 4 and 2
+// bytes (28567 rows of 4111 bf16 with stores of 15 single elements: 262 us)
 template <int DT>
 __device__ __forceinline__ void store_seg(typename Elem<DT>::T *row, int64_t k0, int64_t K, const RawSeg<DT> &r)
 {
-    constexpr int NW = DT == 2 ? 4 : 2;
+    constexpr int NW = DT == 2 ? 4 : 2, E = 16 / NW;         // chunks, elements of one
+    uint8_t *to = reinterpret_cast<uint8_t *>(row + k0);
     if (k0 + 16 <= K) {
 #pragma unroll
-        for (int c = 0; c < NW; c++) *(reinterpret_cast<u32x4 *>(row + k0) + c) = r.w[c];
+        for (int c = 0; c < NW; c++) *(reinterpret_cast<u32x4 *>(to) + c) = r.w[c];
         return;
     }
     if (k0 >= K) return;
-    const int rem = opaque((int)(K - k0));
+    const int rem = opaque((int)(K - k0));                   // 1 .. 15
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        if (i >= rem) continue;
-        if constexpr (DT == 2) reinterpret_cast<uint32_t *>(row + k0)[i] = r.w[i >> 2][i & 3];
-        else row[k0 + i] = (uint16_t)(r.w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
+    for (int c = 0; c < NW; c++) {
+        const int n = rem - E * c;                           // elements of this chunk below K
+        if (n >= E) {
+            *(reinterpret_cast<u32x4 *>(to) + c) = r.w[c];
+        } else if (n > 0) {
+            const int bytes = n * (16 / E);
+            uint32_t w = r.w[c][0];                          // the word after those stored so far
+            uint8_t *at = to + 16 * c;
+            if (bytes & 8) {
+                *reinterpret_cast<uint2 *>(at) = make_uint2(r.w[c][0], r.w[c][1]);
+                w = r.w[c][2];
+                at += 8;
+            }
+            if (bytes & 4) {
+                *reinterpret_cast<uint32_t *>(at) = w;
+                w = (bytes & 8) ? r.w[c][3] : r.w[c][1];
+                at += 4;
+            }
+            if (bytes & 2) *reinterpret_cast<uint16_t *>(at) = (uint16_t)w;
+        }
     }
 }
 
 struct NormWeights { float c[16]; };
 
-// weights of a segment (1 where there are none, 0 past K)
+// weights of a segment (1 where there are none); past K cut_weights follows
 __device__ __forceinline__ void load_weights(const float *w, int64_t k0, int64_t K, NormWeights &n)
 {
     if (w && k0 + 16 <= K) {
@@ -142,6 +181,13 @@ __device__ __forceinline__ void load_weights(const float *w, int64_t k0, int64_t
 #pragma unroll
         for (int i = 0; i < 16; i++) n.c[i] = w[k0 + min(i, rem - 1)];
     }
+}
+
+// 0 past K: an element there is 0, but the weight may be an infinity or a NaN
+__device__ __forceinline__ void cut_weights(int64_t k0, int64_t K, NormWeights &n)
+{
+    if (k0 + 16 <= K) return;
+    const int rem = (int)(K - k0);
 #pragma unroll
     for (int i = 0; i < 16; i++) n.c[i] = i < rem ? n.c[i] : 0.0f;
 }
@@ -245,12 +291,13 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs<DT> a, int64_t
     RawSeg<DT> x = {}, r = {};                       // zero in lanes that hold no row: they store nothing
     auto fetch = [&](int64_t row) {
         if (!active || row >= n_rows) return;
-        fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, x);
-        if constexpr (kRes) fetch_stream<DT>(a.r + row * a.ld_r, k0, a.K, r);
+        fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, row + 1 < n_rows, x);
+        if constexpr (kRes) fetch_stream<DT>(a.r + row * a.ld_r, k0, a.K, row + 1 < n_rows, r);
     };
     const int64_t step = (int64_t)gridDim.x * rpw;
     int64_t base = (int64_t)blockIdx.x * rpw;
     fetch(base + slot);
+    cut_weights(k0, a.K, w);
     int parity = 0;
     // codes are stored after the next row's arrival: a wait for its loads would also wait for
     // stores issued after them
@@ -262,7 +309,9 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormArgs<DT> a, int64_t
         const bool live = active && row < n_rows;
         float v[16], zmax = 0.0f;
         double ss = 0.0;
+        cut_segment<DT>(k0, a.K, x);
         if constexpr (kRes) {
+            cut_segment<DT>(k0, a.K, r);
             add_segment<DT>(x, r);
             if (live && a.sum) store_seg<DT>(a.sum + row * a.ld_sum, k0, a.K, x);
         }
@@ -302,6 +351,10 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
     const int G = blockDim.x >> 4;
     float *tile = lds + grp * kTileStrideF;
     const int slices = (nb + G - 1) / G;
+    auto fetch = [&](const typename Elem<DT>::T *p, int64_t ld, int64_t row, int64_t k0, RawSeg<DT> &seg) {
+        fetch_stream<DT>(p + row * ld, k0, a.K, row + 1 < n_rows, seg);
+        cut_segment<DT>(k0, a.K, seg);
+    };
     int parity = 0;
     for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x) {
         float v[16], zmax = 0.0f;
@@ -310,13 +363,14 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
         for (int s = 0; s < slices; s++) {
             const int64_t k0 = ((int64_t)(s * G + grp) * 16 + t) * 16;
             RawSeg<DT> x, r;
-            fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, x);
+            fetch(a.x, a.ld_x, row, k0, x);
             if constexpr (kRes) {
-                fetch_stream<DT>(a.r + row * a.ld_r, k0, a.K, r);
+                fetch(a.r, a.ld_r, row, k0, r);
                 add_segment<DT>(x, r);
                 if (a.sum) store_seg<DT>(a.sum + row * a.ld_sum, k0, a.K, x);
             }
             load_weights(a.w, k0, a.K, w);
+            cut_weights(k0, a.K, w);
             weigh<DT>(x, w, v, ss);
             hadamard256(v, tile, t, natural != 0);
 #pragma unroll
@@ -332,16 +386,17 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
             const int64_t k0 = ((int64_t)b * 16 + t) * 16;
             RawSeg<DT> x, r;
             if (kRes && a.sum) {
-                fetch_stream<DT>(a.sum + row * a.ld_sum, k0, a.K, x);   // this thread's own stores
+                fetch(a.sum, a.ld_sum, row, k0, x);   // this thread's own stores
             } else {
-                fetch_stream<DT>(a.x + row * a.ld_x, k0, a.K, x);
+                fetch(a.x, a.ld_x, row, k0, x);
                 if constexpr (kRes) {
-                    fetch_stream<DT>(a.r + row * a.ld_r, k0, a.K, r);
+                    fetch(a.r, a.ld_r, row, k0, r);
                     add_segment<DT>(x, r);
                 }
             }
             double unused = 0.0;
             load_weights(a.w, k0, a.K, w);
+            cut_weights(k0, a.K, w);
             weigh<DT>(x, w, v, unused);
             hadamard256(v, tile, t, natural != 0);
             if (b < nb) store_codes<8>(v, rq, out + row * ld_out, b, t);
@@ -366,13 +421,15 @@ static hipError_t launch_norm(const NormArgs<DT> &a, int64_t M, int8_t *out, int
                            M, nb, out, ld_out, scale, natural);
         return hipGetLastError();
     }
-    // rows a workgroup: the fewest rounds over the device, 16 waves of this kernel a compute unit
-    // (short batches: a row each; long ones: the packing that leaves the fewest lanes idle)
+    // rows a workgroup: the fewest rounds over the device, 4 waves of this kernel a SIMD, of which
+    // a workgroup of 4 waves or more takes equally many on each (short batches: a row each; long
+    // ones: the packing that leaves the fewest lanes idle).  25530 rows of 4600 bf16: one row in 5
+    // waves, as 16 waves a compute unit would suggest, 232 us, three in 14 180 us
     int rpw = 1;
     int64_t best = INT64_MAX;
     for (int n = 1; n * nb <= kMaxGroupsWide; n++) {
-        const int waves = (n * nb + 3) / 4;
-        const int64_t at_once = 256 * (int64_t)(16 / waves) * n, rounds = (M + at_once - 1) / at_once;
+        const int waves = (n * nb + 3) / 4, groups = waves < 4 ? 16 / waves : 4 / ((waves + 3) / 4);
+        const int64_t at_once = 256 * (int64_t)groups * n, rounds = (M + at_once - 1) / at_once;
         if (rounds < best) { best = rounds; rpw = n; }
     }
     const int threads = (rpw * nb + 3) / 4 * 64;
