@@ -198,7 +198,12 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b)
 struct Task {
     int b, hk, block, split, part;
 };
-// Key/value heads lie apart by the XCDs' stride; the longest rows (causal) come first.
+// The longest rows (causal) come first.  Workgroups go to the eight XCDs in turn, and a sequence's
+// key/value head stays on one of them where there are eight heads or a multiple: its keys and
+// values are then read into one L2, and every XCD has its share of each sequence.  With other
+// numbers of heads sequences of different lengths would load the XCDs unevenly, so there the
+// units move on by one each row of whole blocks (4 ragged prompts of up to 2000 tokens, 16 query and 2
+// key/value heads of 64: 66 us without, 47 with).
 __device__ __forceinline__ Task task_of(const AttnArgs &a, int id)
 {
     Task t;
@@ -206,12 +211,15 @@ __device__ __forceinline__ Task task_of(const AttnArgs &a, int id)
     t.part = 0;
     int w = id;
     if (id >= a.whole) {
-        t.part = id - a.whole;
-        t.split = t.part / a.tail;
-        w = a.whole + t.part % a.tail;
+        const int i = id - a.whole;
+        t.split = i / a.tail;
+        t.part = i;
+        w = a.whole + i % a.tail;
     }
-    const int units = a.B * a.Hkv, unit = w % units;
-    t.block = a.row_blocks - 1 - w / units;
+    const int units = a.B * a.Hkv, row = w / units;
+    int unit = w % units;
+    if (a.B > 1 && a.Hkv % 8 != 0 && (row + 1) * units <= a.whole) unit = (unit + row) % units;
+    t.block = a.row_blocks - 1 - row;
     t.b = unit / a.Hkv;
     t.hk = unit % a.Hkv;
     return t;
@@ -233,6 +241,14 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 // Software pipeline over halves of a page (32 keys): a step issues the score products of the
 // next half, the softmax of this one under them, this half's second products, and under
 // those the widening of half a page to come; one barrier a step.
+// 32 rows a wave: with 64 a wave reads its operands half as often, but needs 512 registers, and
+// one wave a SIMD has nothing to issue under its products (3.7 ms against 2.85 below).
+// Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.85 ms, 1000 TFLOP/s (a library product
+// of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32 and 8 heads: 406 to 454 us, 800
+// to 890; three sequences of up to 515 new tokens over 10515, 12 heads of 64, fp16: 71 us, bound by the vector units (the
+// softmax of a score costs the same for half the products).  Counters of the first: matrix
+// cores busy 48 % of the cycles, vector units 41, LDS 42 and 6 in bank conflicts, at 1.98 GHz; a
+// wave issues 47 % of its time, waits 30 for a busy unit and 23 for data and at barriers.
 constexpr int kWaves = 4, kRowsBlock = 32 * kWaves;
 
 template <int DT, int D>
@@ -845,13 +861,19 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
         // shares them out).  The FP32 parts are written and read: in the time of a page the device
         // moves about 10 KiB a compute unit.
         const int64_t slots = (D == 64 ? 3 : 2) * (int64_t)cus;
-        int64_t best = (base + slots - 1) / slots * (pages + 3) * 95 / 100;   // splitting has to save 5 %
+        // Of the blocks, those that have rows: full ones, and about half a block a sequence.  Up to 515,
+        // 311 and 106 rows over up to 10515 keys, 12 heads of 64: 73 us by these, 93 by all blocks; 30
+        // sequences of up to 46 rows over 14183, 16 and 4 heads of 128: 166 against 205; the other way
+        // 44 of up to 74 over 1547, 56 and 8 heads of 64: 68 against 61.
+        const int64_t full = Hkv * (T * (Hq / Hkv) / per + (B + 1) / 2), busy = full < base ? (full < 1 ? 1 : full) : base;
+        auto rounds = [&](int64_t blocks) { return ((int64_t)((double)blocks * busy / base) + slots - 1) / slots; };
+        int64_t best = rounds(base) * (pages + 3) * 95 / 100;                 // splitting has to save 5 %
         for (const int64_t whole : {(int64_t)0, base / slots * slots}) {
             const int64_t tail = base - whole;
             if (tail == 0) continue;
             for (int64_t n = 2; n <= pages / 8 && n <= 64; n++) {
-                const int64_t join = 2 * n * tail * kRowsBlock * D * 4 / (10240 * (int64_t)cus);
-                const int64_t cost = whole / slots * (pages + 3) + (tail * n + slots - 1) / slots * ((pages + n - 1) / n + 3) + join;
+                const int64_t join = (int64_t)(2.0 * n * tail * busy / base * kRowsBlock * D * 4 / (10240.0 * cus));
+                const int64_t cost = rounds(whole) * (pages + 3) + rounds(tail * n) * ((pages + n - 1) / n + 3) + join;
                 if (cost < best) {
                     best = cost;
                     p.whole = whole;
