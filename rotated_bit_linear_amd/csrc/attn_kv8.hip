@@ -868,7 +868,7 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
         const int64_t full = Hkv * (T * (Hq / Hkv) / per + (B + 1) / 2), busy = full < base ? (full < 1 ? 1 : full) : base;
         auto rounds = [&](int64_t blocks) { return ((int64_t)((double)blocks * busy / base) + slots - 1) / slots; };
         int64_t best = rounds(base) * (pages + 3) * 95 / 100;                 // splitting has to save 5 %
-        for (const int64_t whole : {(int64_t)0, base / slots * slots}) {
+        for (const int64_t whole : {(int64_t)0, (int64_t)((double)(busy / slots * slots) * base / busy)}) {
             const int64_t tail = base - whole;
             if (tail == 0) continue;
             for (int64_t n = 2; n <= pages / 8 && n <= 64; n++) {
