@@ -243,12 +243,13 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 // those the widening of half a page to come; one barrier a step.
 // 32 rows a wave: with 64 a wave reads its operands half as often, but needs 512 registers, and
 // one wave a SIMD has nothing to issue under its products (3.7 ms against 2.85 below).
-// Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.85 ms, 1000 TFLOP/s (a library product
-// of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32 and 8 heads: 406 to 454 us, 800
-// to 890; three sequences of up to 515 new tokens over 10515, 12 heads of 64, fp16: 71 us, bound by the vector units (the
-// softmax of a score costs the same for half the products).  Counters of the first: matrix
-// cores busy 48 % of the cycles, vector units 41, LDS 42 and 6 in bank conflicts, at 1.98 GHz; a
-// wave issues 47 % of its time, waits 30 for a busy unit and 23 for data and at barriers.
+// Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.82 to 2.87 ms, 1000 TFLOP/s (a library
+// product of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32 and 8 heads: 402 to 459
+// us, 790 to 900; three sequences of up to 515 new tokens over 10515, 12 heads of 64, fp16: 55 us
+// and 12 for the join, bound by the vector units (the softmax of a score costs the same for half
+// the products).  Counters of the first: matrix cores busy 48 % of the cycles, vector units 41,
+// LDS 42 and 6 in bank conflicts, at 1.98 GHz; a wave issues 47 % of its time, waits 30 for a
+// busy unit and 23 for data and at barriers.
 constexpr int kWaves = 4, kRowsBlock = 32 * kWaves;
 
 template <int DT, int D>

@@ -62,9 +62,10 @@ __device__ __forceinline__ void fetch_stream(const typename Elem<DT>::T *row, in
         return;
     }
     if (k0 >= K || more) {
+        const int rem = opaque(k0 < K ? (int)(K - k0) : 0);
 #pragma unroll
         for (int c = 0; c < NW; c++) {
-            if (k0 + 16 / NW * c < K) r.w[c] = *(reinterpret_cast<const u32x4 *>(row + k0) + c);
+            if (16 / NW * c < rem) r.w[c] = *(reinterpret_cast<const u32x4 *>(row + k0) + c);
             else r.w[c] = u32x4{0u, 0u, 0u, 0u};
         }
         return;
@@ -91,7 +92,7 @@ template <int DT>
 __device__ __forceinline__ void cut_segment(int64_t k0, int64_t K, RawSeg<DT> &r)
 {
     if (k0 + 16 <= K || k0 >= K) return;
-    const int rem = (int)(K - k0);                           // 1 .. 15
+    const int rem = opaque((int)(K - k0));                   // 1 .. 15; its comparisons are not kept over the rows
     if constexpr (DT == 2) {
 #pragma unroll
         for (int i = 0; i < 16; i++) r.w[i >> 2][i & 3] = i < rem ? r.w[i >> 2][i & 3] : 0u;

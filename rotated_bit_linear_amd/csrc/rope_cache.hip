@@ -19,8 +19,8 @@
 // are shared by the run.  A team of D/16 lanes holds one token of one head, 8 pairs a lane;
 // the 64 teams of a workgroup cover NT tokens of 64 / NT heads at once, NT from the longest
 // run of new tokens (a single token a sequence leaves a team per head).
-// Measured: 19989 tokens, 56 + 56 + 56 heads of 128, bf16, norms, three axes: 290 to 317 us (4.5 to
-// 4.9 TB/s; a 1 GiB copy runs at 5.1); 7 ragged prompts of up to 1500 tokens, 24 + 8 + 8 heads of
+// Measured: 19989 tokens, 56 + 56 + 56 heads of 128, bf16, norms, three axes: 280 to 317 us (4.5 to
+// 5.1 TB/s; a 1 GiB copy runs at 5.1); 7 ragged prompts of up to 1500 tokens, 24 + 8 + 8 heads of
 // 64: 18 us; 64 single tokens, 32 + 8 + 8 heads of 128: 8 us, a chain of dependent loads.
 #include <hip/hip_runtime.h>
 #include <hip/hip_bf16.h>
