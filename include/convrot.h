@@ -192,6 +192,8 @@ cr_status cr_quant_act_ex(const void *x, cr_dtype x_dtype, int64_t ld_x, int swi
  *   residual   [M, ld_res] of x_dtype, or NULL.
  *   sum        [M, ld_sum] of x_dtype out, or NULL (it must be NULL without a residual).  It
  *              may be x or residual itself, with that operand's row stride.
+ *              Of x and residual the rest of the 16 bytes that hold a row's end may be read
+ *              where another row follows, and does not matter; of sum only [M, K] is written.
  *   weight     [K] float, 4-byte aligned, or NULL for ones.
  *   eps        finite, >= 0.
  *   x_s8, ld_s8, x_scale, flags as in cr_quant_act; rows with K_pad > CR_TWO_PASS_K_PAD

@@ -246,7 +246,7 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 // Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.82 to 2.87 ms, 1000 TFLOP/s (a library
 // product of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32 and 8 heads: 402 to 459
 // us, 790 to 900; three sequences of up to 515 new tokens over 10515, 12 heads of 64, fp16: 55 us
-// and 12 for the join, bound by the vector units (the softmax of a score costs the same for half
+// and 11 for the join, bound by the vector units (the softmax of a score costs the same for half
 // the products).  Counters of the first: matrix cores busy 48 % of the cycles, vector units 41,
 // LDS 42 and 6 in bank conflicts, at 1.98 GHz; a wave issues 47 % of its time, waits 30 for a
 // busy unit and 23 for data and at barriers.
@@ -770,14 +770,14 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
 }
 
 // --------------------------------------------------------------- joining the splits ----
-// W waves per row of the split blocks: the runs that hold keys the row sees, each wave's in order,
-// the waves' sums through LDS.
+// W waves per row of the split blocks: the runs that hold keys the row sees, two (D = 128) or four
+// at a time in 16-byte loads, a fixed order of sums; the waves' sums through LDS.
 template <int DT, int D, int W>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
-    constexpr int E = D / 64;
+    constexpr int L = D / 4, P = 64 / L;                 // lanes of a run's row, runs a wave takes at once
     __shared__ float part[4][D + 1];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), dim = 4 * (lane % L);
     const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;
     const int64_t stride = (int64_t)a.tail * rows;       // rows of one split
     if (id >= stride) return;                            // whole workgroups where waves share a row
@@ -792,32 +792,42 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
     for (int i = lane; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + id].x);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-    float acc[E] = {}, sum = 0.0f;
-#pragma unroll 8
-    for (int i = wave % W; i < n; i += W) {
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int i = wave % W * P + lane / L; i < n; i += W * P) {
         const float2 ml = a.part_ml[i * stride + id];
         const float f = __builtin_amdgcn_exp2f(ml.x - top);
         sum = fmaf(ml.y, f, sum);
+        const f32x4 o = *reinterpret_cast<const f32x4 *>(a.part_o + (i * stride + id) * D + dim);
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(a.part_o[(i * stride + id) * D + E * lane + e], f, acc[e]);
+        for (int e = 0; e < 4; e++) acc[e] = fmaf(o[e], f, acc[e]);
+    }
+#pragma unroll
+    for (int x = L; x < 64; x <<= 1) {
+        sum += __shfl_xor(sum, x);
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[e] += __shfl_xor(acc[e], x);
     }
     if constexpr (W > 1) {
+        if (lane < L) {
 #pragma unroll
-        for (int e = 0; e < E; e++) part[wave][E * lane + e] = acc[e];
+            for (int e = 0; e < 4; e++) part[wave][dim + e] = acc[e];
+        }
         if (lane == 0) part[wave][D] = sum;
         __syncthreads();
         if (wave != 0) return;
 #pragma unroll
         for (int w = 1; w < W; w++) {
 #pragma unroll
-            for (int e = 0; e < E; e++) acc[e] += part[w][E * lane + e];
+            for (int e = 0; e < 4; e++) acc[e] += part[w][dim + e];
             sum += part[w][D];
         }
     }
+    if (lane >= L) return;                               // they hold the same sums
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *po = a.out + (s.t0 + tok) * a.ld_out + (task.hk * a.G + (r - tok * a.G)) * D + E * lane;
-    if constexpr (E == 2) *reinterpret_cast<uint32_t *>(po) = Half<DT>::pack(acc[0] * inv, acc[1] * inv);
-    else *po = (uint16_t)Half<DT>::pack(acc[0] * inv, 0.0f);
+    uint16_t *po = a.out + (s.t0 + tok) * a.ld_out + (task.hk * a.G + (r - tok * a.G)) * D + dim;
+    *reinterpret_cast<u32x2v *>(po) = u32x2v{Half<DT>::pack(acc[0] * inv, acc[1] * inv), Half<DT>::pack(acc[2] * inv, acc[3] * inv)};
 }
 
 // ----------------------------------------------------------------------- launching ----
