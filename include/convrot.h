@@ -555,8 +555,9 @@ typedef struct {
  *            radians, (x, y) -> (x cos - y sin, y cos + x sin) on elements (i, i + D/2), or
  *            (2i, 2i + 1) with CR_FLAG_ROPE_INTERLEAVED; frequency 0 leaves a pair as it is.  An
  *            axis beyond n_axes counts as the last.  The angle is reduced in FP64.
- *   max_new  at least the longest run of new tokens of a sequence (sizes the launch; tokens of
- *            longer runs are not processed).
+ *   max_new  at least the longest run of new tokens of a sequence (sizes the launch; of a longer
+ *            run the first max_new tokens are processed, the others' queries are not written and
+ *            their places in the cache are left as they are).
  * Queries are rounded to dtype.  Keys (rotated, FP32) and values are coded against their page's
  * scale: the smallest power of two >= 2^-126 with which the largest finite magnitude of the
  * page's new tokens is at most 448, or the page's scale so far where that is larger and the

@@ -55,4 +55,46 @@ __host__ __device__ inline int64_t batch_page(const Batch &s, int b, int64_t p)
     return id >= 0 && id < s.n_pages ? id : -1;
 }
 
+// ---- the append's walk: a workgroup takes one page of one sequence ----
+
+// pages that a run of max_new tokens may touch, wherever it starts in its first one
+__host__ __device__ inline int64_t append_visits(int64_t max_new) { return (max_new + kPage - 2) / kPage + 1; }
+
+// log2 of the tokens that a workgroup holds at a time: at least max_new, or a page
+__host__ __device__ inline int append_log_tokens(int64_t max_new)
+{
+    int l = 0;
+    while ((1 << l) < max_new && (1 << l) < kPage) l++;
+    return l;
+}
+
+// the new tokens of a sequence that lie on the visit-th page of its run
+struct PageRun {
+    int64_t page;    // position / kPage
+    int64_t row0;    // row of the first of them
+    int nt, off0;    // how many, and where on the page they start
+    bool stored;     // the cache is long enough to hold the run
+};
+
+// False where there are none.  Of a run longer than max_new the first max_new tokens count: the launch
+// is sized for those, so nt never exceeds the tokens that a workgroup holds.
+__host__ __device__ inline bool append_page_run(const Batch &s, int b, int max_new, int64_t visit, PageRun &r)
+{
+    int64_t t0, n;
+    batch_rows(s, b, t0, n);
+    const int64_t kv = s.kv_lens[b];
+    r.stored = kv >= n;
+    const int64_t first = kv >= n ? kv - n : 0;              // position of the first new token
+    const int m = (int)n < max_new ? (int)n : max_new;      // rows are counted in 31 bits
+    const int64_t end = first + m;
+    r.page = first / kPage + visit;
+    const int64_t lo = first > r.page * kPage ? first : r.page * kPage;
+    const int64_t hi = end < (r.page + 1) * kPage ? end : (r.page + 1) * kPage;
+    if (lo >= hi) return false;
+    r.nt = (int)(hi - lo);
+    r.off0 = (int)(lo - r.page * kPage);
+    r.row0 = t0 + (lo - first);
+    return true;
+}
+
 }  // namespace convrot

@@ -48,7 +48,8 @@ struct RopeArgs {
     Batch batch;
     int n_axes;
     int Hq, Hkv;
-    int visits;          // pages that the longest run of new tokens may touch
+    int max_new;         // tokens of a run that are processed
+    int visits;          // pages that so many tokens may touch
     int log_tokens;      // of NT
     int q_chunks, kv_chunks;   // workgroups that share a page's heads (each takes every so-manieth)
     uint32_t q_blocks;
@@ -177,17 +178,9 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
     const int chunks = is_q ? a.q_chunks : a.kv_chunks;
     const uint32_t id = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
     const int chunk = id % chunks, visit = id / chunks % a.visits, b = id / chunks / a.visits;
-    int64_t t0, n;
-    batch_rows(a.batch, b, t0, n);
-    if (n == 0) return;
-    const int64_t kv = a.batch.kv_lens[b];
-    const int64_t first = kv >= n ? kv - n : 0;            // position of the first new token
-    const int64_t pg = first / kPage + visit;
-    const int64_t lo = first > pg * kPage ? first : pg * kPage;
-    const int64_t hi = first + n < (pg + 1) * kPage ? first + n : (pg + 1) * kPage;
-    if (lo >= hi) return;
-    const int nt = (int)(hi - lo), off0 = (int)(lo - pg * kPage);
-    const int64_t row0 = t0 + (lo - first);
+    PageRun run;
+    if (!append_page_run(a.batch, b, a.max_new, visit, run)) return;
+    const int nt = run.nt, off0 = run.off0;
 
     const int NT = 1 << a.log_tokens, HP = TEAMS >> a.log_tokens;   // tokens and heads at a time
     const int tid = threadIdx.x, c = tid % TEAM, team = tid / TEAM;
@@ -196,9 +189,9 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
     // ---- cosine and sine of this lane's pairs, shared by the workgroup's heads ----
     const float *weight = is_q ? a.q_weight : a.k_weight;
     const bool live = tk < nt;
-    const int64_t row = row0 + tk;
-    const int64_t page = is_q ? 0 : batch_page(a.batch, b, pg);
-    if (!is_q && (kv < n || page < 0)) return;             // nowhere to put them
+    const int64_t row = run.row0 + tk;
+    const int64_t page = is_q ? 0 : batch_page(a.batch, b, run.page);
+    if (!is_q && (!run.stored || page < 0)) return;        // nowhere to put them
     const uint16_t *qkv = static_cast<const uint16_t *>(a.qkv) + row * a.ld_qkv;
     const int step = chunks * HP, h0 = chunk * HP;         // heads h0 + slot, + step, ...
     // the first head's loads, under the sines
@@ -245,11 +238,13 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
     }
     if (is_q) {
         if (!live) return;                                 // whole teams, no barrier on this side
-        uint16_t *out = static_cast<uint16_t *>(a.q_out) + row * a.ld_q;
+        const int64_t at = run.row0 + opaque(tk);          // found again: not kept over the other side's loop
+        const uint16_t *src = static_cast<const uint16_t *>(a.qkv) + at * a.ld_qkv;
+        uint16_t *out = static_cast<uint16_t *>(a.q_out) + at * a.ld_q;
         for (int h = h0 + slot; h < a.Hq; h += step) {
             float x[16];
             decode16<DT, IL>(r0, x);
-            if (h + step < a.Hq) r0 = fetch16<D, IL>(qkv + (h + step) * D, c);
+            if (h + step < a.Hq) r0 = fetch16<D, IL>(src + (h + step) * D, c);
             turn16(x, turn, weight ? team_rstd<D>(x, a.eps) : 1.0f);
             uint16_t *o = out + h * D;
             u32x4v s0, s1;
@@ -301,7 +296,7 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
                 fv = ov / sv;
             }
             __syncthreads();                               // every lane has the old scales
-            const int lane = tk * TEAM + c, lanes = NT * TEAM;   // this head's lanes
+            const int lane = opaque(tk * TEAM + c), lanes = NT * TEAM;   // this head's lanes
             if (fk != 1.0f)
                 for (int i = lane; i < off0 * D; i += lanes) kp[i] = rescale1(kp[i], fk);
             if (fv != 1.0f)
@@ -311,7 +306,8 @@ __global__ __launch_bounds__(4 * D, 4) void rope_append_kernel(RopeArgs a)
                 }
         }
         const float ik = 1.0f / sk, iv = 1.0f / sv;
-        const bool whole = nt == kPage;                    // a full page (then HP is 1): values through LDS
+        // a full page of one head at a time (nt is at most NT, so HP is 1): values through LDS
+        const bool whole = nt == kPage && HP == 1;
         if (on) {
             if (tk == 0 && c == 0) {
                 a.k_scale[at] = sk;
@@ -359,9 +355,10 @@ template <int DT, int D>
 static hipError_t launch_rope(RopeArgs a, int64_t B, int64_t max_new, bool interleaved, int cus, hipStream_t st)
 {
     constexpr int TEAMS = 64;
-    while ((1 << a.log_tokens) < max_new && (1 << a.log_tokens) < kPage) a.log_tokens++;
+    a.max_new = (int)max_new;
+    a.log_tokens = append_log_tokens(max_new);
     const int hp = TEAMS >> a.log_tokens;
-    a.visits = (int)((max_new + kPage - 2) / kPage + 1);
+    a.visits = (int)append_visits(max_new);
     // heads per workgroup: a multiple of those it takes at a time, as many as leave four
     // workgroups for every compute unit (the sines are then shared by more heads), at most 8
     // steps (19989 tokens, 56 heads: 318 us with 16, 301 with 8; 8 heads with 4: 50 us, with 2: 58)
