@@ -417,6 +417,10 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     // Written out in the order of issue: per matrix product the operand AHEAD of it is
     // read, and as much vector work follows as the product takes.
     constexpr int NQ = D / 16, NV = D / 16, AHEAD = D == 64 ? 3 : 4, RING = D == 64 ? 4 : 8;
+    // what the barrier after a step may leave outstanding: operand reads for the next step, but no more
+    // than follow the step's last staging write (its widening ends half way through the second products)
+    constexpr int LEFT = AHEAD < NV / 2 ? AHEAD : NV / 2;
+    static_assert(LEFT <= NV - NV / 2 && LEFT <= AHEAD, "a staging write must not be left outstanding");
     u32x4v f[RING];
     auto step = [&](int kb, const f32x16 &x, f32x16 &y, float c, int bk, int bv, int bk1,
                     auto widen) __attribute__((always_inline)) {
@@ -497,7 +501,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
                 clean_v(vr, p + 1);
                 lds_done();                             // its notes are written
             }
-            barrier_but<AHEAD>();                       // values p are staged; values p - 1 are read
+            barrier_but<LEFT>();                        // values p are staged; values p - 1 are read
             if (tid < 2) nan_keys[(p + 2) % 3][tid] = 0;       // read in page p - 1, written after the next barrier
             step(0, sa, sb, c, cur, cur, nxt, [&](int i) __attribute__((always_inline)) { store_v(vr, nxt, i); });
             load_v(at2, vr);
@@ -507,7 +511,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             }
             mx = both_halves_max(top) * c;
             raise();
-            barrier_but<AHEAD>();                       // keys p + 1 are staged; keys p are read
+            barrier_but<LEFT>();                        // keys p + 1 are staged; keys p are read
             // ---- keys 32..63; the scores of keys 0..31 of page p + 1; keys p + 2 staged ----
             step(1, sb, sa, c, nxt, cur, nxt, [&](int i) __attribute__((always_inline)) { store_k(kr, cur, i); });
             ok = ok1;
