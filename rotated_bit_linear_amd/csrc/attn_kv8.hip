@@ -495,7 +495,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         for (int p = p0; p < pl; p++) {
             const int cur = (p - p0) & 1, nxt = cur ^ 1;
             // ---- keys 0..31 of page p; the scores of its keys 32..63; values p + 1 staged ----
-            take_scale(vs);
+            if (ok) take_scale(vs);                     // page 0 stands in for a missing one: its scale is not this sequence's
             raise();
             if (masked(p + 1, ok1)) {
                 clean_v(vr, p + 1);
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         }
         // ---- the last page ----
         const int cur = (pl - p0) & 1;
-        take_scale(vs);
+        if (ok) take_scale(vs);
         raise();
         __syncthreads();
         step(0, sa, sb, c, cur, cur, cur, [](int) {});
