@@ -578,8 +578,8 @@ cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, in
  *   out[t, h] = sum_j p_j V[j] / sum_j p_j,  p_j = exp(sm_scale * q[t, h] . K[j]),
  * over the keys j < kv_lens[b] of the token's sequence, and with CR_FLAG_CAUSAL only those up
  * to the token's own position kv_lens[b] - (its run's length) + (its index in the run).  Query
- * head h reads key/value head h / (Hq / Hkv).  A token that sees no key gives zeros.  A NaN
- * in a key or value reaches exactly the tokens that see it.
+ * head h reads key/value head h / (Hq / Hkv).  A token that sees no key gives zeros.  A NaN in a
+ * key reaches exactly the tokens that see it, a NaN in a value its one element of those tokens.
  *   q, out   [T, ld_q], [T, ld_out] of dtype (CR_BF16 or CR_FP16), Hq heads of D (64 or 128)
  *            elements; rows of 16-byte multiples, 16-byte aligned.
  *   max_q, max_kv   at least the longest run of queries, and about the longest kv_lens (they

@@ -22,9 +22,10 @@
 // then p is at most 2^8, which FP32 sums and both 16-bit types hold without loss, and the
 // accumulators need no rescaling.
 // Masked places: scores are selected, not added to, so NaN or infinite codes of keys that a
-// row does not see leave it alone; values beyond kv_len are zeroed, and where some row of
-// the tile does not see a key whose value holds a NaN code, the codes are zeroed and the NaN
-// put into the scores of the rows that do see it.
+// row does not see leave it alone; values beyond kv_len are zeroed.  On a page that every row of the
+// tile sees whole, a NaN code goes through the product into its element.  On any other page NaN
+// codes are zeroed before the product, and where there were some, such pages are read again at the
+// end and the elements of the rows that see them set to NaN.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -118,12 +119,23 @@ __device__ __forceinline__ u32x4v widen8(uint32_t lo, uint32_t hi)
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 // 0xFF in those bytes
 __device__ __forceinline__ uint32_t spread_bytes(uint32_t b) { return (b << 1) - (b >> 7); }
-// one bit a byte (bits 0..3)
-__device__ __forceinline__ uint32_t gather_bits(uint32_t b) { return (((b >> 7) & 0x01010101u) * 0x01020408u) >> 24; }
 // the bytes of a word that hold tokens below `left` (word w of a run of tokens)
 __device__ __forceinline__ uint32_t below_bytes(int left)
 {
     return left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+}
+
+// whether the first `left` tokens of one dim (64 codes) hold a NaN code
+__device__ __forceinline__ bool nan_among(const uint8_t *codes, int left)
+{
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < kPage / 16; i++) {
+        const u32x4v c = *reinterpret_cast<const u32x4v *>(codes + 16 * i);
+#pragma unroll
+        for (int w = 0; w < 4; w++) bad |= nan_bytes(c[w] & below_bytes(left - 16 * i - 4 * w));
+    }
+    return bad != 0;
 }
 
 // the larger of the two lanes l and l ^ 32, in both
@@ -260,7 +272,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     constexpr int ROWS = kRowsBlock;
     __shared__ __attribute__((aligned(16))) uint8_t ldsK[2][kPage * KROW];
     __shared__ __attribute__((aligned(16))) uint8_t ldsV[2][D * VROW];
-    __shared__ uint32_t nan_keys[3][2];                 // keys of a tile whose values hold NaN codes
+    __shared__ uint32_t nan_codes;                      // NaN codes were cleared from a page
 
     const Task task = task_of(a, blockIdx.x);
     const int b = task.b, hk = task.hk;
@@ -322,21 +334,21 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         *reinterpret_cast<u32x4v *>(ldsV[buf] + ((tid >> 2) + 64 * (i >> 1)) * VROW + 32 * (tid & 3) + 16 * (i & 1)) =
             widen8<1>(r[i >> 1][i & 1], r[i >> 1][2 + (i & 1)]);
     };
-    // values of a page that some row does not see whole: nothing beyond the cache, NaN codes
-    // cleared and noted
+    // values of a page that some row does not see whole: nothing beyond the cache, no NaN codes
     auto clean_v = [&](u32x4v (&r)[VQ], int p) __attribute__((always_inline)) {
+        uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < VQ; i++) {
-            const int j = tid & 3;
-            const int left = s.kv - p * kPage - 16 * j;
+            const int left = s.kv - p * kPage - 16 * (tid & 3);
 #pragma unroll
             for (int w = 0; w < 4; w++) {
                 const uint32_t x = r[i][w] & below_bytes(left - 4 * w);
                 const uint32_t bad = nan_bytes(x);
-                if (bad) atomicOr(&nan_keys[p % 3][j >> 1], gather_bits(bad) << (16 * (j & 1) + 4 * w));
+                any |= bad;
                 r[i][w] = x & ~spread_bytes(bad);
             }
         }
+        if (any) nan_codes = 1;
     };
 
     // ---- the parts of a page ----
@@ -356,14 +368,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         return *reinterpret_cast<const u32x4v *>(ldsV[buf] + lane_v + 32 * d * VROW + 32 * (2 * kb + j));
     };
     auto mask = [&](f32x16 &x, int p, int kb, bool ok) __attribute__((always_inline)) {
-        const uint32_t bad = nan_keys[p % 3][kb] >> (4 * half);
         const int left = (ok ? lim - p * kPage : 0) - 32 * kb - 4 * half;
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-            const int key = 8 * (e >> 2) + (e & 3);
-            const float y = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : x[e];
-            x[e] = key < left ? y : -__builtin_inff();
-        }
+        for (int e = 0; e < 16; e++) x[e] = 8 * (e >> 2) + (e & 3) < left ? x[e] : -__builtin_inff();
     };
     float top;                                          // largest score of the half page so far
     auto max_of = [&](const f32x16 &x, int e0, int e1) __attribute__((always_inline)) {
@@ -453,7 +460,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         l = fmaf(sum, weight, l);
     };
 
-    if (tid < 6) (&nan_keys[0][0])[tid] = 0;
+    if (tid == 0) nan_codes = 0;
     __syncthreads();
     if (p0 < p1) {
         u32x4v kr[KQ], vr[VQ];
@@ -499,10 +506,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             raise();
             if (masked(p + 1, ok1)) {
                 clean_v(vr, p + 1);
-                lds_done();                             // its notes are written
+                lds_done();                             // its note is written
             }
             barrier_but<LEFT>();                        // values p are staged; values p - 1 are read
-            if (tid < 2) nan_keys[(p + 2) % 3][tid] = 0;       // read in page p - 1, written after the next barrier
             step(0, sa, sb, c, cur, cur, nxt, [&](int i) __attribute__((always_inline)) { store_v(vr, nxt, i); });
             load_v(at2, vr);
             if (masked(p, ok)) {
@@ -546,6 +552,23 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
 #pragma unroll
         for (int i = 0; i < NV; i++)
             o[i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[i / (D / 32)], o[i % (D / 32)]);
+        if (__builtin_expect(nan_codes != 0, 0)) {      // uniform; the notes lie before the last barrier
+            uint64_t hit = 0;                           // bit 16 d + e: element e of o[d]
+            for (int q = max(p0, lim_all / kPage); q < p1; q++) {
+                bool there;
+                const int64_t page = page_of(table[q], there);
+                if (!there) continue;
+                const int left = lim - q * kPage;
+                for (int i = 0; i < D / 2; i++) {
+                    const int dim = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
+                    if (nan_among(a.v + (page * D + dim) * kPage, left)) hit |= (uint64_t)1 << i;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[d][e] = (hit >> (16 * d + e)) & 1 ? __builtin_nanf("") : o[d][e];
+        }
     }
 
     // ---- the lane's row (found again rather than kept): dims 32 d + 8 g + 4 half + 0..3 ----
@@ -657,6 +680,7 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
 #pragma unroll
     for (int d = 0; d < D / 16; d++) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kLow, l = 0.0f, vref = kMinScale;
+    bool nan_codes = false;                              // NaN codes were cleared from a page of this wave
 
     for (int p = p0 + wave; p < p1; p += 4) {
         if (there(id)) {                                 // uniform in the wave
@@ -671,28 +695,21 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
                 }
             }
             if ((p + 1) * kPage > lim_all) {                 // some row does not see all of the page
-                uint32_t bad = 0;                            // this lane's 16 keys whose values hold NaN codes
+                uint32_t bad = 0;
                 const int inside = s.kv - p * kPage - 16 * quarter;
 #pragma unroll
                 for (int d = 0; d < D / 16; d++)
 #pragma unroll
                     for (int w = 0; w < 4; w++) {
-                        uint32_t x = vr[d][w] & below_bytes(inside - 4 * w);
+                        const uint32_t x = vr[d][w] & below_bytes(inside - 4 * w);
                         const uint32_t n = nan_bytes(x);
-                        bad |= gather_bits(n) << (4 * w);
+                        bad |= n;
                         vr[d][w] = x & ~spread_bytes(n);
                     }
-#pragma unroll
-                for (int x = 1; x < 16; x <<= 1) bad |= __shfl_xor(bad, x);   // over the dims of the other lanes
+                nan_codes |= __builtin_amdgcn_ballot_w64(bad != 0) != 0;
                 const int left = lim - p * kPage - 16 * quarter;
 #pragma unroll
-                for (int kb = 0; kb < 4; kb++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int key = 4 * kb + e;
-                        const float x = (bad >> key) & 1 ? __uint_as_float(0x7fc00000u) : sc[kb][e];
-                        sc[kb][e] = key < left ? x : -__builtin_inff();
-                    }
+                for (int e = 0; e < 16; e++) sc[e >> 2][e & 3] = e < left ? sc[e >> 2][e & 3] : -__builtin_inff();
             }
             const float c = score_factor(a.factor, ks);
             float mx = sc[0][0];
@@ -735,6 +752,21 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
         id = id1;
         load_page(id);
         id1 = entry((int64_t)p + 8);                     // a page ahead of its use
+    }
+
+    if (__builtin_expect(nan_codes, 0)) {                // uniform in the wave
+        uint32_t hit = 0;                                // bit 4 d + e: element e of o[d]
+        for (int p = p0 + wave; p < p1; p += 4) {
+            const int32_t at = entry(p);
+            if ((p + 1) * kPage <= lim_all || !there(at)) continue;
+            const uint8_t *vp = a.v + ((int64_t)at * a.Hkv + hk) * (kPage * D);
+            for (int i = 0; i < D / 4; i++)
+                if (nan_among(vp + (16 * (i >> 2) + 4 * quarter + (i & 3)) * kPage, lim - p * kPage)) hit |= 1u << i;
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; d++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[d][e] = (hit >> (4 * d + e)) & 1 ? __builtin_nanf("") : o[d][e];
     }
 
     // ---- join the waves: row `col`, dims 16 d + 4 quarter .. ----
