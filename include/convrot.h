@@ -516,7 +516,7 @@ cr_status cr_gemm_nvfp4_fused(const int8_t *a_s8, int64_t lda, const float *a_sc
  *   k        [n_pages, Hkv, CR_KV8_PAGE, D] bytes, 16-byte aligned.
  *   v        [n_pages, Hkv, D, CR_KV8_PAGE] bytes, 16-byte aligned (dim-major).
  *   k_scale, v_scale   [n_pages, Hkv] float, positive.  cr_rope_append_kv8 writes powers of
- *            two; cr_attn_kv8 takes any positive scales.
+ *            two; cr_attn_kv8 takes any positive finite scales.
  *   n_pages  pages in the cache.
  *   page_table   [B, ld_table] int32: page p of sequence b holds its tokens p * CR_KV8_PAGE ..;
  *            ld_table is also the most pages a sequence may have (at most CR_KV8_MAX_PAGES).
@@ -588,9 +588,10 @@ cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, in
  *   Hq       a multiple of Hkv.      sm_scale   finite, > 0.
  *   workspace   cr_attn_kv8_workspace_bytes(...) bytes (for the current device), 256-byte
  *            aligned; may be NULL where that is 0.  Nothing in it needs to start at zero.
- * Products are accumulated and softmax statistics held in FP32; probabilities are rounded to
- * dtype for the second product.  The cache may be split into runs that are joined at the end;
- * the result does not depend on timing.
+ * Products are accumulated and softmax statistics held in FP32.  For the second product
+ * probabilities are rounded to FP16, whatever dtype is: off by at most 2^-11 of themselves, or
+ * 2^-25 of the row's largest where that is more, for every page whatever its value scale.  The
+ * cache may be split into runs that are joined at the end; the result does not depend on timing.
  */
 size_t cr_attn_kv8_workspace_bytes(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, int64_t Hkv,
                                    int64_t D);

@@ -14,10 +14,12 @@
 // are FP32.  P is rounded to fp16 whatever the queries' type (half a step is at most 2^-11 of
 // p, and 2^-25 below 2^-14; the second product takes the codes as fp16): in bf16, half a
 // step is 2^-8, and a row that one key dominates would be off by that twice.
-// Scales: a page's key scale joins the factor of the exponent's argument, its value scale
-// the exponent: P holds p * vs / vref, vref the largest value scale so far (the accumulators
-// are rescaled when it grows), so 16-bit P never overflows.  A value scale below 2^-64 vref
-// counts as 2^-64 vref.
+// Scales: a page's key scale joins the factor of the exponent's argument, its value scale vs
+// the exponent: P holds p * vs / 2^at, and a row's accumulators sums of p v / 2^at.  `at` follows the
+// smallest scale so far (2^at <= vs, so P is at least p and loses no more bits than p would);
+// it rises where a row's own P would leave fp16 (2^14), and stays where the row's accumulators would
+// pass 2^100, beside which the page does not count.  It is a power of two, so that moving it
+// rounds nothing, and each row has its own: what one row weighs takes no bits from another.
 // The running maximum is only raised when some row's scores exceed it by 8 (in log2): until
 // then p is at most 2^8, which FP32 sums and both 16-bit types hold without loss, and the
 // accumulators need no rescaling.
@@ -186,9 +188,52 @@ typedef const __attribute__((address_space(4))) float *scalar_f32;
 
 constexpr float kLow = -1e30f;    // running maximum before the first key
 constexpr float kSlack = 8.0f;    // log2: how far scores may exceed the running maximum
+constexpr float kMostP = 14.0f;   // log2 of the largest P
 
 // the factor of a page's scores and the shift of its exponents
 __device__ __forceinline__ float score_factor(float factor, float ks) { return fmaxf(factor * ks, 1e-37f); }
+
+// A row's reference for the values: its accumulators hold sums of p v / 2^at.  The lanes of a row hold
+// the same; where all rows of the wave do, a page is compared with it by one scalar.
+struct ValueRef {
+    int at = 128;                 // above any scale: the first page's is taken
+    int common = kNone;           // `at` of every lane, or kNone
+    int exp = 128;                // the current page's scale: 2^(exp + frac), 0 <= frac < 1 (uniform)
+    float frac = 0.0f;
+    float shift = 0.0f;           // log2 of its ratio to 2^at, joins the exponents
+    float weight = 1.0f;          // what turns the page's sum of P into a sum of p
+    static constexpr int kNone = 1 << 20;
+    __device__ __forceinline__ void page(float vs)
+    {
+        vs = fmaxf(vs, 0x1p-149f);
+        exp = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(vs) - 1);
+        frac = __builtin_amdgcn_logf(2.0f * __builtin_amdgcn_frexp_mantf(vs));
+        aim();
+    }
+    __device__ __forceinline__ void aim()
+    {
+        // below -64 P is zero in any case, and its FP32 sum still holds p
+        shift = fmaxf(frac + (float)(exp - at), -64.0f);
+        weight = __builtin_amdgcn_exp2f(-shift);
+    }
+    // false: for every row 2^at is at most the page's scale, and P stays below 2^kMostP
+    __device__ __forceinline__ bool stray() const { return (uint32_t)(exp - common) >= (uint32_t)(kMostP - kSlack); }
+    // whether a row's scores (at most `over` above its maximum) ask for another `at`
+    __device__ __forceinline__ bool off(float over) const { return exp < at || over + shift > kMostP; }
+    // moves `at` down to the page's scale, as far as accumulators of magnitude `top` allow, or up to
+    // it where its largest P would exceed 2^kMostP; returns by how many powers of two they grow
+    __device__ __forceinline__ int move(float top, float over)
+    {
+        const int room = top > 0.0f ? max(100 - __builtin_amdgcn_frexp_expf(top), 0) : 1024;
+        const int from = at;
+        if (exp < at) at = max(exp, at - room);
+        else if (over + shift > kMostP) at = exp;
+        const int first = __builtin_amdgcn_readfirstlane(at);
+        common = __builtin_amdgcn_ballot_w64(at != first) == 0 ? first : kNone;
+        aim();
+        return from - at;
+    }
+};
 
 // per-sequence facts of a workgroup (the launch's limits keep n * G and the keys within an int)
 struct Seq {
@@ -357,7 +402,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int e = 0; e < 16; e++) o[d][e] = 0.0f;
-    float m = kLow, l = 0.0f, mx = 0.0f, vref = kMinScale;
+    float m = kLow, l = 0.0f, mx = 0.0f;
+    ValueRef ref;
     // operand i of the score products with 32 keys (half kb of a tile), of the second products
     const int lane_k = col * KROW + 16 * half, lane_v = col * VROW + 16 * half;
     auto read_k = [&](int buf, int kb, int i) __attribute__((always_inline)) {
@@ -378,41 +424,40 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         for (int e = e0; e < e1; e++) top = e == 0 ? x[0] : fmaxf(top, x[e]);
         stay(top);
     };
-    auto rescale = [&](float f) __attribute__((always_inline)) {
-#pragma unroll
-        for (int d = 0; d < D / 32; d++)
-#pragma unroll
-            for (int e = 0; e < 16; e++) o[d][e] *= f;
-    };
-    // the maximum of the scores about to be added: rescales what is there where it grows (rare)
+    // the maximum of the scores about to be added, and the reference of their values: rescales
+    // what is there where they move (rare)
     auto raise = [&]() __attribute__((always_inline)) {
-        if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0, 0)) {
             const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
             m = m1;
             l *= f;
-            rescale(f);
+#pragma unroll
+            for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) o[d][e] *= f;
         }
-    };
-    // the value scale of the page about to be added, likewise: its shift of the exponents and
-    // weight in the sum
-    float shift = 0.0f, weight = 1.0f;
-    auto take_scale = [&](float vs) __attribute__((always_inline)) {
-        const float vsx = fmaxf(fmaxf(vs, kMinScale), vref * 0x1p-64f);
-        if (vsx > vref) {                               // uniform
-            const float f = vref * __builtin_amdgcn_rcpf(vsx);
-            vref = vsx;
-            rescale(f);
+        if (__builtin_expect(ref.stray(), 0)) {
+            if (__builtin_amdgcn_ballot_w64(ref.off(mx - m)) != 0) {
+                float most = 0.0f;
+#pragma unroll
+                for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) most = fmaxf(most, fabsf(o[d][e]));
+                const int by = ref.move(both_halves_max(most), mx - m);
+#pragma unroll
+                for (int d = 0; d < D / 32; d++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) o[d][e] = __builtin_amdgcn_ldexpf(o[d][e], by);
+            }
         }
-        shift = __builtin_amdgcn_logf(vsx) - __builtin_amdgcn_logf(vref);
-        weight = vref * __builtin_amdgcn_rcpf(vsx);
     };
     u32x4v pk[2];
     float sum;
     auto softmax = [&](const f32x16 &x, float c, int e0, int e1) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = e0; e < e1; e += 2) {
-            const float y = __builtin_amdgcn_exp2f(fmaf(x[e], c, shift - m));
-            const float z = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c, shift - m));
+            const float y = __builtin_amdgcn_exp2f(fmaf(x[e], c, ref.shift - m));
+            const float z = __builtin_amdgcn_exp2f(fmaf(x[e + 1], c, ref.shift - m));
             sum = e == 0 ? y + z : sum + (y + z);
             pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(y, z);
         }
@@ -457,7 +502,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             __builtin_amdgcn_sched_barrier(0);
         }
         __builtin_amdgcn_s_setprio(0);
-        l = fmaf(sum, weight, l);
+        l = fmaf(sum, ref.weight, l);
     };
 
     if (tid == 0) nan_codes = 0;
@@ -471,7 +516,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         int64_t at = page_of(table[p0], ok), at1 = page_of(table[min(p0 + 1, pl)], ok1);
         int64_t at2 = page_of(table[min(p0 + 2, pl)], ok2);
         int32_t id3 = table[min(p0 + 3, pl)];
-        float c = score_factor(a.factor, a.k_scale[at]), vs = a.v_scale[at];
+        float c = score_factor(a.factor, a.k_scale[at]);
+        // page 0 stands in for a page that is not there: its scale is not this sequence's
+        if (ok) ref.page(a.v_scale[at]);
         float ks1 = a.k_scale[at1], vs1 = a.v_scale[at1];
         f32x16 sa, sb;
         {
@@ -502,7 +549,6 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         for (int p = p0; p < pl; p++) {
             const int cur = (p - p0) & 1, nxt = cur ^ 1;
             // ---- keys 0..31 of page p; the scores of its keys 32..63; values p + 1 staged ----
-            if (ok) take_scale(vs);                     // page 0 stands in for a missing one: its scale is not this sequence's
             raise();
             if (masked(p + 1, ok1)) {
                 clean_v(vr, p + 1);
@@ -522,7 +568,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             step(1, sb, sa, c, nxt, cur, nxt, [&](int i) __attribute__((always_inline)) { store_k(kr, cur, i); });
             ok = ok1;
             c = score_factor(a.factor, ks1);
-            vs = vs1;
+            if (ok) ref.page(vs1);
             if (masked(p + 1, ok)) {
                 mask(sa, p + 1, 0, ok);
                 max_of(sa, 0, 16);
@@ -537,7 +583,6 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         }
         // ---- the last page ----
         const int cur = (pl - p0) & 1;
-        if (ok) take_scale(vs);
         raise();
         __syncthreads();
         step(0, sa, sb, c, cur, cur, cur, [](int) {});
@@ -548,7 +593,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         mx = both_halves_max(top) * c;
         raise();
         softmax(sb, c, 0, 16);
-        l = fmaf(sum, weight, l);
+        l = fmaf(sum, ref.weight, l);
 #pragma unroll
         for (int i = 0; i < NV; i++)
             o[i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[i / (D / 32)], o[i % (D / 32)]);
@@ -575,6 +620,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     const float total = l + __shfl_xor(l, 32);
     const int r = r0 + opaque_lane(wave * 32 + col);
     if (r >= s.rows) return;
+    auto value = [&](float x) __attribute__((always_inline)) { return __builtin_amdgcn_ldexpf(x, ref.at); };
     if (task.split >= 0) {
         const int64_t at = (int64_t)task.part * ROWS + (r - r0);
         float *po = a.part_o + at * D;
@@ -583,19 +629,19 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
 #pragma unroll
             for (int g = 0; g < 4; g++)
                 *reinterpret_cast<f32x4 *>(po + 32 * d + 8 * g + 4 * half) =
-                    f32x4{o[d][4 * g] * vref, o[d][4 * g + 1] * vref, o[d][4 * g + 2] * vref, o[d][4 * g + 3] * vref};
+                    f32x4{value(o[d][4 * g]), value(o[d][4 * g + 1]), value(o[d][4 * g + 2]), value(o[d][4 * g + 3])};
         if (half == 0) a.part_ml[at] = float2{m, total};
         return;
     }
-    const float inv = total == 0.0f ? 0.0f : vref / total;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     uint16_t *po = a.out + (s.t0 + r / a.G) * a.ld_out + (hk * a.G + r % a.G) * D;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int g = 0; g < 4; g++)
             *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
-                u32x2v{Half<DT>::pack(o[d][4 * g] * inv, o[d][4 * g + 1] * inv),
-                       Half<DT>::pack(o[d][4 * g + 2] * inv, o[d][4 * g + 3] * inv)};
+                u32x2v{Half<DT>::pack(value(o[d][4 * g] * inv), value(o[d][4 * g + 1] * inv)),
+                       Half<DT>::pack(value(o[d][4 * g + 2] * inv), value(o[d][4 * g + 3] * inv))};
 }
 
 // ------------------------------------------------------------- single tokens: few rows ----
@@ -679,7 +725,8 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
     f32x4 o[D / 16];
 #pragma unroll
     for (int d = 0; d < D / 16; d++) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = kLow, l = 0.0f, vref = kMinScale;
+    float m = kLow, l = 0.0f;
+    ValueRef ref;
     bool nan_codes = false;                              // NaN codes were cleared from a page of this wave
 
     for (int p = p0 + wave; p < p1; p += 4) {
@@ -717,21 +764,30 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
             for (int e = 1; e < 16; e++) mx = fmaxf(mx, sc[e >> 2][e & 3]);
             mx = fmaxf(mx, __shfl_xor(mx, 16));
             mx = fmaxf(mx, __shfl_xor(mx, 32)) * c;
-            if (__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0) {
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(mx > m + kSlack) != 0, 0)) {
                 const float m1 = fmaxf(m, mx), f = __builtin_amdgcn_exp2f(m - m1);
                 m = m1;
                 l *= f;
 #pragma unroll
                 for (int d = 0; d < D / 16; d++) o[d] *= f;
             }
-            const float vsx = fmaxf(fmaxf(vs, kMinScale), vref * 0x1p-64f);
-            if (vsx > vref) {                                // uniform
-                const float f = vref / vsx;
-                vref = vsx;
+            ref.page(vs);
+            if (__builtin_expect(ref.stray(), 0)) {
+                if (__builtin_amdgcn_ballot_w64(ref.off(mx - m)) != 0) {
+                    float most = 0.0f;
 #pragma unroll
-                for (int d = 0; d < D / 16; d++) o[d] *= f;
+                    for (int d = 0; d < D / 16; d++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) most = fmaxf(most, fabsf(o[d][e]));
+                    most = fmaxf(most, __shfl_xor(most, 16));
+                    const int by = ref.move(fmaxf(most, __shfl_xor(most, 32)), mx - m);
+#pragma unroll
+                    for (int d = 0; d < D / 16; d++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) o[d][e] = __builtin_amdgcn_ldexpf(o[d][e], by);
+                }
             }
-            const float shift = __builtin_amdgcn_logf(vsx / vref) - m;
+            const float shift = ref.shift - m;
             float sum = 0.0f;
             u32x4v pk[2];
 #pragma unroll
@@ -741,7 +797,7 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
                 sum += x + y;
                 pk[e >> 3][(e >> 1) & 3] = Half<1>::pack(x, y);
             }
-            l = fmaf(sum, vref / vsx, l);
+            l = fmaf(sum, ref.weight, l);
 #pragma unroll
             for (int d = 0; d < D / 16; d++) {
                 o[d] = Half<1>::mfma16(widen8<1>(vr[d][0], vr[d][1]), pk[0], o[d]);
@@ -775,7 +831,8 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
 #pragma unroll
     for (int d = 0; d < D / 16; d++)
         *reinterpret_cast<f32x4 *>(&lo[wave][col][16 * d + 4 * quarter]) =
-            f32x4{o[d][0] * vref, o[d][1] * vref, o[d][2] * vref, o[d][3] * vref};
+            f32x4{__builtin_amdgcn_ldexpf(o[d][0], ref.at), __builtin_amdgcn_ldexpf(o[d][1], ref.at),
+                  __builtin_amdgcn_ldexpf(o[d][2], ref.at), __builtin_amdgcn_ldexpf(o[d][3], ref.at)};
     if (quarter == 0) { lm[wave][col] = m; ll[wave][col] = l; }
     __syncthreads();
     const int n_rows = last - r0 + 1;

@@ -5,8 +5,8 @@
 // bytes (dim-major: the 16 consecutive tokens of one dim that a lane of the P V product needs
 // are then one 16-byte load), E4M3 codes (OCP: bias 7, largest 448, 0x7F and 0xFF NaN).  One
 // FP32 scale per page and kv head for the keys and one for the values: value = code * scale.
-// The writer's scales are powers of two, so that a page whose scale grows is rescaled without
-// rounding (but for codes that fall below E4M3's normal range).
+// The writer's scales are powers of two (2^-126 for a page of zeros), so that a page whose scale grows
+// is rescaled without rounding (but for codes that fall below E4M3's normal range).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,7 +15,6 @@
 namespace convrot {
 
 constexpr int kPage = 64;
-constexpr float kMinScale = 0x1p-126f;   // the scale of a page that holds zeros only
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
