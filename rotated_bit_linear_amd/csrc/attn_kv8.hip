@@ -58,8 +58,8 @@ struct AttnArgs {
     int64_t pages_per_split;
     float factor;            // sm_scale * log2(e)
     int causal;
-    float *part_o;           // of each split block [split][tail][rows of a block][D]: sums of p v
-    float2 *part_ml;         // [split][tail][rows of a block] (running maximum, sum)
+    float *part_o;           // of each split block [split][tail][rows of a block][D]: a run's own result
+    float2 *part_ml;         // [split][tail][rows of a block] (its maximum, its sum of p)
 };
 
 // 16-bit operand types: bf16 (0) or fp16 (1)
@@ -620,7 +620,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     const float total = l + __shfl_xor(l, 32);
     const int r = r0 + opaque_lane(wave * 32 + col);
     if (r >= s.rows) return;
-    auto value = [&](float x) __attribute__((always_inline)) { return __builtin_amdgcn_ldexpf(x, ref.at); };
+    // the average first, then its power of two: sums of p v may pass FP32 where their average does not
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    auto value = [&](float x) __attribute__((always_inline)) { return __builtin_amdgcn_ldexpf(x * inv, ref.at); };
     if (task.split >= 0) {
         const int64_t at = (int64_t)task.part * ROWS + (r - r0);
         float *po = a.part_o + at * D;
@@ -633,15 +635,14 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
         if (half == 0) a.part_ml[at] = float2{m, total};
         return;
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     uint16_t *po = a.out + (s.t0 + r / a.G) * a.ld_out + (hk * a.G + r % a.G) * D;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
 #pragma unroll
         for (int g = 0; g < 4; g++)
             *reinterpret_cast<u32x2v *>(po + 32 * d + 8 * g + 4 * half) =
-                u32x2v{Half<DT>::pack(value(o[d][4 * g] * inv), value(o[d][4 * g + 1] * inv)),
-                       Half<DT>::pack(value(o[d][4 * g + 2] * inv), value(o[d][4 * g + 3] * inv))};
+                u32x2v{Half<DT>::pack(value(o[d][4 * g]), value(o[d][4 * g + 1])),
+                       Half<DT>::pack(value(o[d][4 * g + 2]), value(o[d][4 * g + 3]))};
 }
 
 // ------------------------------------------------------------- single tokens: few rows ----
@@ -825,28 +826,35 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
             for (int e = 0; e < 4; e++) o[d][e] = (hit >> (4 * d + e)) & 1 ? __builtin_nanf("") : o[d][e];
     }
 
-    // ---- join the waves: row `col`, dims 16 d + 4 quarter .. ----
+    // ---- join the waves' averages: row `col`, dims 16 d + 4 quarter .. ----
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    const float mean = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-    for (int d = 0; d < D / 16; d++)
-        *reinterpret_cast<f32x4 *>(&lo[wave][col][16 * d + 4 * quarter]) =
-            f32x4{__builtin_amdgcn_ldexpf(o[d][0], ref.at), __builtin_amdgcn_ldexpf(o[d][1], ref.at),
-                  __builtin_amdgcn_ldexpf(o[d][2], ref.at), __builtin_amdgcn_ldexpf(o[d][3], ref.at)};
+    for (int d = 0; d < D / 16; d++) {
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = __builtin_amdgcn_ldexpf(o[d][e] * mean, ref.at);
+        *reinterpret_cast<f32x4 *>(&lo[wave][col][16 * d + 4 * quarter]) = x;
+    }
     if (quarter == 0) { lm[wave][col] = m; ll[wave][col] = l; }
     __syncthreads();
     const int n_rows = last - r0 + 1;
     for (int i = tid; i < n_rows * (D / 2); i += 256) {
         const int rr = i / (D / 2), d = 2 * (i % (D / 2));
-        float top = kLow, x = 0.0f, y = 0.0f, sum = 0.0f;
+        float top = kLow, x = 0.0f, y = 0.0f, sum = 0.0f, f[4];
 #pragma unroll
         for (int w = 0; w < 4; w++) top = fmaxf(top, lm[w][rr]);
 #pragma unroll
         for (int w = 0; w < 4; w++) {
-            const float f = __builtin_amdgcn_exp2f(lm[w][rr] - top);
-            x = fmaf(lo[w][rr][d], f, x);
-            y = fmaf(lo[w][rr][d + 1], f, y);
-            sum = fmaf(ll[w][rr], f, sum);
+            f[w] = ll[w][rr] * __builtin_amdgcn_exp2f(lm[w][rr] - top);
+            sum += f[w];
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int w = 0; w < 4; w++) {
+            x = fmaf(lo[w][rr][d], f[w] * inv, x);
+            y = fmaf(lo[w][rr][d + 1], f[w] * inv, y);
         }
         const int gr = r0 + rr, tok = gr / a.G;
         const int hd = hk * a.G + (gr - tok * a.G);
@@ -855,9 +863,7 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
             *reinterpret_cast<float2 *>(a.part_o + at * D + d) = float2{x, y};
             if (d == 0) a.part_ml[at] = float2{top, sum};
         } else {
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            *reinterpret_cast<uint32_t *>(a.out + (s.t0 + tok) * a.ld_out + (int64_t)hd * D + d) =
-                Half<DT>::pack(x * inv, y * inv);
+            *reinterpret_cast<uint32_t *>(a.out + (s.t0 + tok) * a.ld_out + (int64_t)hd * D + d) = Half<DT>::pack(x, y);
         }
     }
 }
@@ -869,7 +875,7 @@ template <int DT, int D, int W>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 {
     constexpr int L = D / 4, P = 64 / L;                 // lanes of a run's row, runs a wave takes at once
-    __shared__ float part[4][D + 1];
+    __shared__ float part[4][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), dim = 4 * (lane % L);
     const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;
     const int64_t stride = (int64_t)a.tail * rows;       // rows of one split
@@ -881,24 +887,31 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
     const int tok = r / a.G;
     const int64_t pages = (visible(a, s, tok) + kPage - 1) / kPage;
     const int n = (int)min((pages + a.pages_per_split - 1) / a.pages_per_split, (int64_t)a.splits);
-    float top = kLow;
-    for (int i = lane; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + id].x);
+    // the first 64 runs' maxima and sums stay in the lanes
+    const float2 own = lane < n ? a.part_ml[lane * stride + id] : float2{kLow, 0.0f};
+    float top = own.x;
+    for (int i = lane + 64; i < n; i += 64) top = fmaxf(top, a.part_ml[i * stride + id].x);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    float sum = own.y * __builtin_amdgcn_exp2f(own.x - top);
+    for (int i = lane + 64; i < n; i += 64) {
+        const float2 ml = a.part_ml[i * stride + id];
+        sum = fmaf(ml.y, __builtin_amdgcn_exp2f(ml.x - top), sum);
+    }
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    float sum = 0.0f;
 #pragma unroll 4
     for (int i = wave % W * P + lane / L; i < n; i += W * P) {
         const float2 ml = a.part_ml[i * stride + id];
-        const float f = __builtin_amdgcn_exp2f(ml.x - top);
-        sum = fmaf(ml.y, f, sum);
+        const float f = ml.y * __builtin_amdgcn_exp2f(ml.x - top) * inv;
         const f32x4 o = *reinterpret_cast<const f32x4 *>(a.part_o + (i * stride + id) * D + dim);
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[e] = fmaf(o[e], f, acc[e]);
     }
 #pragma unroll
     for (int x = L; x < 64; x <<= 1) {
-        sum += __shfl_xor(sum, x);
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[e] += __shfl_xor(acc[e], x);
     }
@@ -907,20 +920,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
 #pragma unroll
             for (int e = 0; e < 4; e++) part[wave][dim + e] = acc[e];
         }
-        if (lane == 0) part[wave][D] = sum;
         __syncthreads();
         if (wave != 0) return;
 #pragma unroll
-        for (int w = 1; w < W; w++) {
+        for (int w = 1; w < W; w++)
 #pragma unroll
             for (int e = 0; e < 4; e++) acc[e] += part[w][dim + e];
-            sum += part[w][D];
-        }
     }
     if (lane >= L) return;                               // they hold the same sums
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *po = a.out + (s.t0 + tok) * a.ld_out + (task.hk * a.G + (r - tok * a.G)) * D + dim;
-    *reinterpret_cast<u32x2v *>(po) = u32x2v{Half<DT>::pack(acc[0] * inv, acc[1] * inv), Half<DT>::pack(acc[2] * inv, acc[3] * inv)};
+    *reinterpret_cast<u32x2v *>(po) = u32x2v{Half<DT>::pack(acc[0], acc[1]), Half<DT>::pack(acc[2], acc[3])};
 }
 
 // ----------------------------------------------------------------------- launching ----
