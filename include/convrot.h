@@ -586,8 +586,12 @@ cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, in
  *            size the launch; queries of longer runs get no output, longer caches only lose
  *            balance).
  *   Hq       a multiple of Hkv.      sm_scale   finite, > 0.
- *   workspace   cr_attn_kv8_workspace_bytes(...) bytes (for the current device), 256-byte
- *            aligned; may be NULL where that is 0.  Nothing in it needs to start at zero.
+ *   workspace   cr_attn_kv8_workspace_bytes(...) bytes, asked for with the sizes of this very call
+ *            (and for the current device): how the cache is split depends on all of them, so a
+ *            smaller T, B or max_q may need more than a larger one.  256-byte aligned; may be NULL
+ *            where that is 0.  Nothing in it needs to start at zero.  It grows with the rows that
+ *            there are, not with max_q: at most 64 * T * Hq * (D + 2) floats, or 40 MiB where
+ *            that is more.
  * Products are accumulated and softmax statistics held in FP32.  For the second product
  * probabilities are rounded to FP16, whatever dtype is: off by at most 2^-11 of themselves, or
  * 2^-25 of the row's largest where that is more, for every page whatever its value scale.  The

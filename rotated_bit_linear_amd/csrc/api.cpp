@@ -1092,7 +1092,7 @@ cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, in
     }
     if (!any || max_q == 0) return CR_OK;
     if (p.whole > convrot::kMostBlocks || p.whole + p.tail * p.splits > convrot::kMostBlocks ||
-        T > 4 * convrot::kMostBlocks / Hq)
+        p.join_groups > convrot::kMostBlocks || T > 4 * convrot::kMostBlocks / Hq)
         return CR_ERR_TOO_LARGE;
     if ((s = current_device_ok()) != CR_OK) return s;
     convrot::AttnLaunch l{};

@@ -58,8 +58,10 @@ struct AttnArgs {
     int64_t pages_per_split;
     float factor;            // sm_scale * log2(e)
     int causal;
-    float *part_o;           // of each split block [split][tail][rows of a block][D]: a run's own result
-    float2 *part_ml;         // [split][tail][rows of a block] (its maximum, its sum of p)
+    float *part_o;           // of the split blocks' rows [split][part_rows][D]: a run's own result
+    float2 *part_ml;         // [split][part_rows] (its maximum, its sum of p)
+    int64_t part_rows;       // rows of the split blocks, or of the whole batch (by_token)
+    int by_token;            // a row's part lies at its token and head, not at its place in the block
 };
 
 // 16-bit operand types: bf16 (0) or fp16 (1)
@@ -251,7 +253,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int b)
     return s;
 }
 // what a workgroup does: block `block` of the rows of sequence b and key/value head hk; the whole
-// cache (split < 0), or its run `split` (part: where that goes)
+// cache (split < 0), or its run `split` (part: which of the split blocks it is)
 struct Task {
     int b, hk, block, split, part;
 };
@@ -270,8 +272,8 @@ __device__ __forceinline__ Task task_of(const AttnArgs &a, int id)
     if (id >= a.whole) {
         const int i = id - a.whole;
         t.split = i / a.tail;
-        t.part = i;
-        w = a.whole + i % a.tail;
+        t.part = i % a.tail;
+        w = a.whole + t.part;
     }
     const int units = a.B * a.Hkv, row = w / units;
     int unit = w % units;
@@ -280,6 +282,40 @@ __device__ __forceinline__ Task task_of(const AttnArgs &a, int id)
     t.b = unit / a.Hkv;
     t.hk = unit % a.Hkv;
     return t;
+}
+
+// where the result of a run for row r (r0 the block's first, `per` its rows) goes
+__device__ __forceinline__ int64_t part_of(const AttnArgs &a, const Task &t, const Seq &s, int r, int r0, int per)
+{
+    const int tok = r / a.G;
+    const int64_t at = a.by_token ? (s.t0 + tok) * a.Hq + t.hk * a.G + (r - tok * a.G) : (int64_t)t.part * per + (r - r0);
+    return t.split * a.part_rows + at;
+}
+
+// the sequence that token t belongs to, or -1: of those that begin at or before it the last,
+// sought by 64 lanes at once; where the bounds are not in order, one after the other
+__device__ __forceinline__ int sequence_of(const AttnArgs &a, int64_t t, int lane)
+{
+    auto holds = [&](int b) __attribute__((always_inline)) {
+        int64_t t0, n;
+        batch_rows(a.batch, b, t0, n);
+        return t >= t0 && t < t0 + n;
+    };
+    int lo = 0, n = a.B;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const bool begun = lane * step < n && a.batch.cu[lo + lane * step] <= t;
+        const int k = max(__popcll(__builtin_amdgcn_ballot_w64(begun)) - 1, 0);
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    if (holds(lo)) return lo;
+    for (int b = 0; b < a.B; b += 64) {
+        const uint64_t found = __builtin_amdgcn_ballot_w64(b + lane < a.B && holds(b + lane));
+        if (found) return b + __builtin_ctzll(found);
+    }
+    return -1;
 }
 
 // number of keys that token i of the sequence sees
@@ -624,7 +660,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     auto value = [&](float x) __attribute__((always_inline)) { return __builtin_amdgcn_ldexpf(x * inv, ref.at); };
     if (task.split >= 0) {
-        const int64_t at = (int64_t)task.part * ROWS + (r - r0);
+        const int64_t at = part_of(a, task, s, r, r0, ROWS);
         float *po = a.part_o + at * D;
 #pragma unroll
         for (int d = 0; d < D / 32; d++)
@@ -859,7 +895,7 @@ __global__ __launch_bounds__(256, 3) void attn_few_kernel(AttnArgs a)
         const int gr = r0 + rr, tok = gr / a.G;
         const int hd = hk * a.G + (gr - tok * a.G);
         if (task.split >= 0) {
-            const int64_t at = (int64_t)task.part * kFewRows + rr;
+            const int64_t at = part_of(a, task, s, gr, r0, kFewRows);
             *reinterpret_cast<float2 *>(a.part_o + at * D + d) = float2{x, y};
             if (d == 0) a.part_ml[at] = float2{top, sum};
         } else {
@@ -878,13 +914,28 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows)
     __shared__ float part[4][D];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), dim = 4 * (lane % L);
     const int64_t id = (int64_t)blockIdx.x * (4 / W) + wave / W;
-    const int64_t stride = (int64_t)a.tail * rows;       // rows of one split
+    const int64_t stride = a.part_rows;
     if (id >= stride) return;                            // whole workgroups where waves share a row
-    const Task task = task_of(a, a.whole + (int)(id / rows));
+    Task task;
+    int tok, r;
+    if (a.by_token) {
+        const int t = (int)((uint32_t)id / (uint32_t)a.Hq), head = (int)id - t * a.Hq, units = a.B * a.Hkv;
+        task.b = sequence_of(a, t, lane);
+        if (task.b < 0) return;
+        task.hk = head / a.G;
+        tok = t - a.batch.cu[task.b];
+        r = tok * a.G + head - task.hk * a.G;
+        // in a block that the launch has, and one of the split ones (those are not moved on)
+        const int block = r / rows;
+        if (block >= a.row_blocks) return;
+        if ((int64_t)(a.row_blocks - 1 - block) * units + task.b * a.Hkv + task.hk < a.whole) return;
+    } else {
+        task = task_of(a, a.whole + (int)(id / rows));
+        r = task.block * rows + (int)(id % rows);
+        tok = r / a.G;
+    }
     const Seq s = load_seq(a, task.b);
-    const int r = task.block * rows + (int)(id % rows);
     if (r >= s.rows) return;
-    const int tok = r / a.G;
     const int64_t pages = (visible(a, s, tok) + kPage - 1) / kPage;
     const int n = (int)min((pages + a.pages_per_split - 1) / a.pages_per_split, (int64_t)a.splits);
     // the first 64 runs' maxima and sums stay in the lanes
@@ -999,8 +1050,20 @@ AttnPlan plan_attn_kv8(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int 
     if (p.tail > 0) {
         p.pages_per_split = (pages + p.splits - 1) / p.splits;
         p.splits = (pages + p.pages_per_split - 1) / p.pages_per_split;
-        p.off_ml = (size_t)p.splits * (size_t)p.tail * per * D * 4;
-        p.bytes = p.off_ml + (size_t)p.splits * (size_t)p.tail * per * 8;
+        // Parts lie in the order of the blocks, whose rows the join finds without a search.  Blocks are
+        // counted for the longest run of queries, so a long prompt among short ones may have many times
+        // more than there are rows: above 16 MiB, parts then lie by token and head (one prompt of 2048
+        // tokens and 63 single ones, 32 and 8 heads of 128, over 32768: 3.7 GB by blocks, 0.18 so; 5
+        // sequences of up to 4 tokens over 7997, 96 and 12 heads of 64: 30 us by blocks, 24 so).
+        const int64_t row = (int64_t)p.splits * (D + 2) * 4;
+        p.part_rows = p.tail * per;
+        p.by_token = p.part_rows > T * Hq && p.part_rows > (16 << 20) / row;
+        if (p.by_token) p.part_rows = T * Hq;
+        p.off_ml = (size_t)p.splits * (size_t)p.part_rows * D * 4;
+        p.bytes = (size_t)p.part_rows * (size_t)row;
+        // many runs: four waves a row
+        p.join_waves = p.splits > 8 ? 4 : 1;
+        p.join_groups = p.join_waves == 4 ? p.part_rows : (p.part_rows + 3) / 4;
     }
     return p;
 }
@@ -1009,16 +1072,15 @@ template <int DT, int D>
 static hipError_t launch_attn(const AttnArgs &a, const AttnPlan &p, hipStream_t st)
 {
     const int64_t blocks = p.whole + p.tail * p.splits;
-    if (blocks > kMostBlocks) return hipErrorInvalidValue;
+    if (blocks > kMostBlocks || p.join_groups > kMostBlocks) return hipErrorInvalidValue;
     if (p.few) hipLaunchKernelGGL((attn_few_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     else hipLaunchKernelGGL((attn_rows_kernel<DT, D>), dim3((unsigned)blocks), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.tail == 0) return e;
     const int rows = p.few ? kFewRows : kRowsBlock;
-    // many runs: four waves a row
-    const int64_t n = p.tail * rows;
-    if (p.splits > 8) hipLaunchKernelGGL((attn_join_kernel<DT, D, 4>), dim3((unsigned)n), dim3(256), 0, st, a, rows);
-    else hipLaunchKernelGGL((attn_join_kernel<DT, D, 1>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, st, a, rows);
+    const dim3 grid((unsigned)p.join_groups);
+    if (p.join_waves == 4) hipLaunchKernelGGL((attn_join_kernel<DT, D, 4>), grid, dim3(256), 0, st, a, rows);
+    else hipLaunchKernelGGL((attn_join_kernel<DT, D, 1>), grid, dim3(256), 0, st, a, rows);
     return hipGetLastError();
 }
 
@@ -1036,6 +1098,8 @@ hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st)
     a.pages_per_split = l.plan.pages_per_split;
     a.factor = l.sm_scale * 1.4426950408889634f;
     a.causal = l.causal;
+    a.part_rows = l.plan.part_rows;
+    a.by_token = l.plan.by_token;
     a.part_o = static_cast<float *>(l.workspace);
     a.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(l.workspace) + l.plan.off_ml);
     if (l.D == 128) return l.dtype == 0 ? launch_attn<0, 128>(a, l.plan, st) : launch_attn<1, 128>(a, l.plan, st);

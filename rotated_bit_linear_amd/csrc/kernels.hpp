@@ -125,7 +125,11 @@ struct AttnPlan {
     int64_t row_blocks;      // blocks a sequence and kv head
     int64_t whole, tail;     // blocks that one workgroup does, and blocks split over the cache
     int64_t splits, pages_per_split;
-    size_t off_ml, bytes;    // workspace of the split blocks: partial outputs, then (maximum, sum) pairs
+    int64_t part_rows;       // rows of partial results of one split,
+    bool by_token;           // one for each token and head of the batch, or for each row of the split blocks
+    int join_waves;          // waves that join a row
+    int64_t join_groups;     // workgroups of the join
+    size_t off_ml, bytes;    // workspace: partial outputs, then (maximum, sum) pairs
 };
 // workgroups of 256 threads that a dispatch's 32-bit work-item count allows
 constexpr int64_t kMostBlocks = (int64_t)(UINT32_MAX / 256);
