@@ -188,7 +188,7 @@ __device__ __forceinline__ u32x4v load_codes(const uint8_t *base, uint32_t off)
 typedef const __attribute__((address_space(4))) int32_t *scalar_i32;
 typedef const __attribute__((address_space(4))) float *scalar_f32;
 
-constexpr float kLow = -1e30f;    // running maximum before the first key
+constexpr float kLow = -3.4028235e38f;   // running maximum before the first key: below no finite score
 constexpr float kSlack = 8.0f;    // log2: how far scores may exceed the running maximum
 constexpr float kMostP = 14.0f;   // log2 of the largest P
 
