@@ -192,8 +192,8 @@ constexpr float kLow = -3.4028235e38f;   // running maximum before the first key
 constexpr float kSlack = 8.0f;    // log2: how far scores may exceed the running maximum
 constexpr float kMostP = 14.0f;   // log2 of the largest P
 
-// the factor of a page's scores and the shift of its exponents
-__device__ __forceinline__ float score_factor(float factor, float ks) { return fmaxf(factor * ks, 1e-37f); }
+// the factor of a page's scores: above zero, so that a masked score stays minus infinity
+__device__ __forceinline__ float score_factor(float factor, float ks) { return fmaxf(factor * ks, 0x1p-149f); }
 
 // A row's reference for the values: its accumulators hold sums of p v / 2^at.  The lanes of a row hold
 // the same; where all rows of the wave do, a page is compared with it by one scalar.

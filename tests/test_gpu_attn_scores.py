@@ -43,3 +43,23 @@ def test_all_scores_far_below_zero(new, D, size):
     check(batch, cache, q, torch.ones(100, dtype=torch.float64))
     cache.k_scale[batch.page(0, 1)] = 2.0
     check(batch, cache, q, (torch.arange(100) < PAGE).double())
+
+
+@pytest.mark.parametrize("new", NEW)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [2.0 ** -110, 2.0 ** -124, 2.0 ** -126, 2.0 ** -127])
+def test_small_key_scales(new, D, scale):
+    """Scores of 0 and 2 (of 1 for the last scale) from large queries on keys with the smallest scales."""
+    batch = Batch([1], [PAGE], seed=72)
+    cache = random_cache(batch.n_pages, 1, D, 73, spread=0)
+    i = batch.page(0, 0)
+    cache.k.zero_()
+    cache.k[i, 0, ::3, 5] = torch.tensor(256.0).to(F8).view(torch.uint8).item()
+    cache.k_scale.fill_(scale)
+    top = min(2.0 ** 119, 2.0 ** -7 / scale)
+    q = torch.zeros(new, D, dtype=torch.bfloat16, device=dev())
+    q[:, 5] = top
+    say(f"key scale {scale} new={new} D={D}")
+    p = torch.ones(PAGE, dtype=torch.float64)
+    p[::3] = torch.tensor(top * 256 * scale, dtype=torch.float64).exp()
+    check(batch, cache, q, p)
