@@ -107,14 +107,25 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
 // (a, b) -> r (a ca - b sb, b cb + a sa)
 struct Turn { float ca[8], sa[8], cb[8], sb[8]; };
 
-// 1 / sqrt(mean(x^2) + eps) of the head that a team holds
+// 1 / sqrt(mean(x^2) + eps) of the head that a team holds.  Where FP32 squares overflow or vanish (bf16
+// and eps reach there), x is moved by a power of two first, and eps with it.
 template <int D>
-__device__ __forceinline__ float team_rstd(const float (&x)[16], float eps)
+__device__ __forceinline__ float team_rstd(float (&x)[16], float eps)
 {
-    float s = 0.0f;
+    auto mean = [&]() __attribute__((always_inline)) {
+        float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; i++) s = fmaf(x[i], x[i], s);
-    return 1.0f / sqrtf(team_sum<D / 16>(s) * (1.0f / D) + eps);
+        for (int i = 0; i < 16; i++) s = fmaf(x[i], x[i], s);
+        return team_sum<D / 16>(s) * (1.0f / D);
+    };
+    float m = mean() + eps;
+    if (__builtin_expect(!(m >= 0x1p-100f && m <= 0x1p100f), 0)) {
+        const float k = m < 1.0f ? 0x1p70f : 0x1p-70f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) x[i] *= k;
+        m = mean() + eps * k * k;
+    }
+    return 1.0f / sqrtf(m);
 }
 
 __device__ __forceinline__ void turn16(float (&x)[16], const Turn &t, float r)
