@@ -161,14 +161,19 @@ struct LayerPlan {
 
 inline size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
+std::atomic<int> g_cus[kMaxDevices];       // 0 unknown (asked for once a device: 0.15 us a call)
+
 int current_cus()
 {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
+    int dev = -1, cus = 0;
+    if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices &&
+        (cus = g_cus[dev].load(std::memory_order_relaxed)) > 0)
+        return cus;
+    if (dev < 0 || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) {
         (void)hipGetLastError();
         return 256;
     }
+    if (dev < kMaxDevices) g_cus[dev].store(cus, std::memory_order_relaxed);
     return cus;
 }
 
@@ -477,7 +482,7 @@ cr_status cr_quant_act_rmsnorm(const void *x, cr_dtype x_dtype, int64_t ld_x, co
     return from_hip(convrot::launch_quant_act_rmsnorm(x, (int)x_dtype, ld_x, residual, ld_res, sum, ld_sum, weight,
                                                       eps, M, K, x_s8, ld_s8, x_scale,
                                                       (flags & CR_FLAG_FORCE_TWO_PASS) != 0,
-                                                      (flags & CR_FLAG_BLOCK_TRANSPOSED) != 0, stream));
+                                                      (flags & CR_FLAG_BLOCK_TRANSPOSED) != 0, current_cus(), stream));
 }
 
 cr_status cr_swiglu(const void *h, cr_dtype h_dtype, int64_t ld_h, int64_t M, int64_t F,

@@ -24,7 +24,8 @@ hipError_t launch_quant_act_swiglu(const void *h, int dtype, int64_t ld_h, int64
 // residual addition (r nullptr: none; sum nullptr: not kept), RMS norm and S8 preparation
 hipError_t launch_quant_act_rmsnorm(const void *x, int dtype, int64_t ld_x, const void *r, int64_t ld_r, void *sum,
                                     int64_t ld_sum, const float *w, float eps, int64_t M, int64_t K, int8_t *x_s8,
-                                    int64_t ld_s8, float *x_scale, bool two_pass, bool transposed, hipStream_t st);
+                                    int64_t ld_s8, float *x_scale, bool two_pass, bool transposed, int cus,
+                                    hipStream_t st);
 
 hipError_t launch_swiglu(const void *h, int dtype, int64_t ld_h, int64_t M, int64_t F, float *out,
                          int64_t ld_out, hipStream_t st);

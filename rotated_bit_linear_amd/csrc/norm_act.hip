@@ -411,7 +411,7 @@ __global__ __launch_bounds__(1024) void norm_two_pass_kernel(NormArgs<DT> a, int
 
 template <int DT, bool kRes>
 static hipError_t launch_norm(const NormArgs<DT> &a, int64_t M, int8_t *out, int64_t ld_out, float *scale,
-                              bool force_two_pass, bool natural, hipStream_t st)
+                              bool force_two_pass, bool natural, int cus, hipStream_t st)
 {
     const int nb = (int)((a.K + 255) / 256);
     if (force_two_pass || nb > kMaxGroupsWide) {
@@ -430,7 +430,7 @@ static hipError_t launch_norm(const NormArgs<DT> &a, int64_t M, int8_t *out, int
     int64_t best = INT64_MAX;
     for (int n = 1; n * nb <= kMaxGroupsWide; n++) {
         const int waves = (n * nb + 3) / 4, groups = waves < 4 ? 16 / waves : 4 / ((waves + 3) / 4);
-        const int64_t at_once = 256 * (int64_t)groups * n, rounds = (M + at_once - 1) / at_once;
+        const int64_t at_once = (int64_t)cus * groups * n, rounds = (M + at_once - 1) / at_once;
         if (rounds < best) { best = rounds; rpw = n; }
     }
     const int threads = (rpw * nb + 3) / 4 * 64;
@@ -446,23 +446,24 @@ static hipError_t launch_norm(const NormArgs<DT> &a, int64_t M, int8_t *out, int
 template <int DT>
 static hipError_t launch_norm_dt(const void *x, int64_t ld_x, const void *r, int64_t ld_r, void *sum, int64_t ld_sum,
                                  const float *w, float eps, int64_t M, int64_t K, int8_t *out, int64_t ld_out,
-                                 float *scale, bool two_pass, bool natural, hipStream_t st)
+                                 float *scale, bool two_pass, bool natural, int cus, hipStream_t st)
 {
     using T = typename Elem<DT>::T;
     const NormArgs<DT> a{static_cast<const T *>(x), static_cast<const T *>(r), static_cast<T *>(sum), w, ld_x, ld_r,
                          ld_sum, K, (double)eps};
-    return r ? launch_norm<DT, true>(a, M, out, ld_out, scale, two_pass, natural, st)
-             : launch_norm<DT, false>(a, M, out, ld_out, scale, two_pass, natural, st);
+    return r ? launch_norm<DT, true>(a, M, out, ld_out, scale, two_pass, natural, cus, st)
+             : launch_norm<DT, false>(a, M, out, ld_out, scale, two_pass, natural, cus, st);
 }
 
 hipError_t launch_quant_act_rmsnorm(const void *x, int dtype, int64_t ld_x, const void *r, int64_t ld_r, void *sum,
                                     int64_t ld_sum, const float *w, float eps, int64_t M, int64_t K, int8_t *x_s8,
-                                    int64_t ld_s8, float *x_scale, bool two_pass, bool transposed, hipStream_t st)
+                                    int64_t ld_s8, float *x_scale, bool two_pass, bool transposed, int cus,
+                                    hipStream_t st)
 {
     switch (dtype) {
-    case 0: return launch_norm_dt<0>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, st);
-    case 1: return launch_norm_dt<1>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, st);
-    case 2: return launch_norm_dt<2>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, st);
+    case 0: return launch_norm_dt<0>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, cus, st);
+    case 1: return launch_norm_dt<1>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, cus, st);
+    case 2: return launch_norm_dt<2>(x, ld_x, r, ld_r, sum, ld_sum, w, eps, M, K, x_s8, ld_s8, x_scale, two_pass, !transposed, cus, st);
     default: return hipErrorInvalidValue;
     }
 }
