@@ -135,9 +135,17 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object: 0.2 us a call against 2.8 of the public way,
+# where a short call takes 11.  The names are not public, so a torch without them has the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
-    if stream is None:                             # the current stream's handle, without a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        if _raw_stream is None or _raw_device is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_raw_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
