@@ -583,8 +583,8 @@ cr_status cr_rope_append_kv8(const void *qkv, cr_dtype dtype, int64_t ld_qkv, in
  *   q, out   [T, ld_q], [T, ld_out] of dtype (CR_BF16 or CR_FP16), Hq heads of D (64 or 128)
  *            elements; rows of 16-byte multiples, 16-byte aligned.
  *   max_q, max_kv   at least the longest run of queries, and about the longest kv_lens (they
- *            size the launch; queries of longer runs get no output, longer caches only lose
- *            balance).
+ *            size the launch; of a longer run only the first max_q queries are sure of an output,
+ *            longer caches only lose balance).
  *   Hq       a multiple of Hkv.      sm_scale   finite, > 0.
  *   workspace   cr_attn_kv8_workspace_bytes(...) bytes, asked for with the sizes of this very call
  *            (and for the current device): how the cache is split depends on all of them, so a

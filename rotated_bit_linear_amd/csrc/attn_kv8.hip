@@ -21,8 +21,8 @@
 // pass 2^100, beside which the page does not count.  It is a power of two, so that moving it
 // rounds nothing, and each row has its own: what one row weighs takes no bits from another.
 // The running maximum is only raised when some row's scores exceed it by 8 (in log2): until
-// then p is at most 2^8, which FP32 sums and both 16-bit types hold without loss, and the
-// accumulators need no rescaling.
+// then p is at most 2^8, which FP32 sums and fp16 hold without loss, and the accumulators need
+// no rescaling.
 // Masked places: scores are selected, not added to, so NaN or infinite codes of keys that a
 // row does not see leave it alone; values beyond kv_len are zeroed.  On a page that every row of the
 // tile sees whole, a NaN code goes through the product into its element.  On any other page NaN
@@ -333,16 +333,19 @@ __device__ __forceinline__ int visible(const AttnArgs &a, const Seq &s, int i)
 // lanes of a read cover all banks.
 // Software pipeline over halves of a page (32 keys): a step issues the score products of the
 // next half, the softmax of this one under them, this half's second products, and under
-// those the widening of half a page to come; one barrier a step.
+// those the writes of half a page to come into LDS; one barrier a step.  That half page's codes
+// are converted in front of the first product, with the wait for their loads: waves that only
+// stage share the conversions, and the compiler moves them above the branch.
 // 32 rows a wave: with 64 a wave reads its operands half as often, but needs 512 registers, and
 // one wave a SIMD has nothing to issue under its products (3.7 ms against 2.85 below).
-// Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.82 to 2.87 ms, 1000 TFLOP/s (a library
-// product of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32 and 8 heads: 402 to 459
-// us, 790 to 900; three sequences of up to 515 new tokens over 10515, 12 heads of 64, fp16: 55 us
-// and 11 for the join, bound by the vector units (the softmax of a score costs the same for half
-// the products).  Counters of the first: matrix cores busy 48 % of the cycles, vector units 41,
-// LDS 42 and 6 in bank conflicts, at 1.98 GHz; a wave issues 47 % of its time, waits 30 for a
-// busy unit and 23 for data and at barriers.
+// Measured: 19989 tokens on 19989, 14 heads of 128, bf16: 2.81 to 3.00 ms on different boxes, 950 to
+// 1020 TFLOP/s (a library product of 8192^3 bf16: 1434); causal prompts of up to 4096 tokens, 32
+// and 8 heads: 381 to 416 us, 870 to 950; three sequences of up to 515 new tokens over 10515, 12
+// heads of 64, fp16: 55 us and 9 for the join, bound by the vector units (the softmax of a score
+// costs the same for half the products).  Counters of the first: matrix cores busy 50 % of the
+// cycles, vector units 50 (an exponential takes two slots), LDS 44 and 6 in bank conflicts: the two
+// units' work follows more than it overlaps.  A wave issues 49 % of its time, waits 31 for a busy
+// unit and 20 for data and at barriers.
 constexpr int kWaves = 4, kRowsBlock = 32 * kWaves;
 
 template <int DT, int D>
@@ -635,11 +638,11 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
             o[i % (D / 32)] = Half<1>::mfma32(read_v(cur, 1, i), pk[i / (D / 32)], o[i % (D / 32)]);
         if (__builtin_expect(nan_codes != 0, 0)) {      // uniform; the notes lie before the last barrier
             uint64_t hit = 0;                           // bit 16 d + e: element e of o[d]
-            for (int q = max(p0, lim_all / kPage); q < p1; q++) {
+            for (int pg = max(p0, lim_all / kPage); pg < p1; pg++) {
                 bool there;
-                const int64_t page = page_of(table[q], there);
+                const int64_t page = page_of(table[pg], there);
                 if (!there) continue;
-                const int left = lim - q * kPage;
+                const int left = lim - pg * kPage;
                 for (int i = 0; i < D / 2; i++) {
                     const int dim = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * half + (i & 3);
                     if (nan_among(a.v + (page * D + dim) * kPage, left)) hit |= (uint64_t)1 << i;
@@ -694,9 +697,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void attn_rows_kernel(AttnArg
 // page after it asked for by an id that is there already.  Values are read once by whole cache
 // lines, past the caches; a load of K takes halves of lines (D = 128), whose other halves
 // non-temporal loads would fetch again: 384 us, with both so 405, with neither 413.
-// Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32768 tokens 660 us (6.5 TB/s),
-// of up to 32768 tokens 382 us (6.0); one of 131072 49 us (5.4), of 4097 12 us with its join
-// (8 and 4, both a launch and four dependent loads long).
+// Measured, 32 query and 8 key/value heads of 128: 64 sequences of 32768 tokens 653 us (6.6 TB/s),
+// of up to 32768 tokens 382 us (6.0); one of 131072 47 us (54 on inputs that change), of 4097 12 us
+// with its join (8 and 4, both a launch and four dependent loads long).
 constexpr int kFewRows = 16;
 
 template <int DT, int D>
