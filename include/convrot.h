@@ -102,7 +102,11 @@ enum {
     CR_FLAG_FORCE_TWO_PASS = 1,   /* stream rows twice whatever their length */
     CR_FLAG_BLOCK_TRANSPOSED = 2, /* S8 codes in block-transposed column order (below) */
     CR_FLAG_CAUSAL = 16,          /* cr_attn_kv8: a token sees the keys up to its own */
-    CR_FLAG_ROPE_INTERLEAVED = 32 /* cr_rope_append_kv8: pairs (2i, 2i + 1), not (i, i + D/2) */
+    CR_FLAG_ROPE_INTERLEAVED = 32, /* cr_rope_append_kv8: pairs (2i, 2i + 1), not (i, i + D/2) */
+    CR_FLAG_ROUTE_SIGMOID = 64,   /* cr_route_experts: sigmoid scores, not softmax */
+    CR_FLAG_ROUTE_RENORM = 128,   /* cr_route_experts: weights over the sum of the chosen scores */
+    CR_FLAG_EXPERTS_SCATTER = 256, /* cr_gemm_s8s4_experts: place i writes row rows[i], not row i */
+    CR_FLAG_EXPERTS_SWIGLU = 512  /* cr_gemm_s8s4_experts: SwiGLU of the halves of the columns */
 };
 
 /* Column order of the S8 outputs of the preparation calls.  Default (natural): column k
@@ -604,6 +608,120 @@ cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, in
                       int64_t Hq, int64_t Hkv, int64_t D, const cr_kv8_cache *cache, float sm_scale,
                       void *out, int64_t ld_out, void *workspace, size_t ws_bytes, uint32_t flags,
                       hipStream_t stream);
+
+/*
+ * A layer of experts: T tokens, each with top_k choices among experts.  A slot is one choice of one
+ * token: slot t * top_k + j is choice j of token t.  The calls below are the router (logits to choices
+ * and weights), the plan (slots sorted by expert), the experts' products on the 4-bit weights, the
+ * weighted sum back to tokens, and the last four as one call.  Choices and counts stay on the device,
+ * so that a captured launch serves every step.  At most CR_MAX_EXPERTS experts, CR_MAX_CHOICES choices
+ * a token and 2147483647 slots (CR_ERR_INVALID_ARG beyond).
+ * Experts may be dealt out over devices: a device that holds experts first .. first + E - 1 passes
+ * `first` and its own E weights to the plan and the sum, and choices of other experts (and negative
+ * ones: a token that is padding) count as nothing there.
+ */
+#define CR_MAX_EXPERTS 512
+#define CR_MAX_CHOICES 32
+#define CR_MAX_EXPERT_GROUPS 64
+
+/*
+ * Router: the top_k experts of each token and their weights.
+ *   logits   [T, ld] of dtype (CR_BF16, CR_FP16 or CR_FP32), E of them a row; element-aligned.
+ *   Scores s = softmax over the row's E logits, or sigmoid of each with CR_FLAG_ROUTE_SIGMOID, in FP64.
+ *   An expert's key is s + bias with a bias (for balance: it chooses, and does not weigh), otherwise
+ *   its logit.  A logit of -inf or NaN, or a key of -inf or NaN, is never chosen; +inf takes the
+ *   limit of the scores.
+ *   bias     [E] float, or NULL.
+ *   n_groups (1 .. CR_MAX_EXPERT_GROUPS, a divisor of E), top_groups (1 .. n_groups): the experts are
+ *            n_groups runs of equal length, and only those of the top_groups best runs can be chosen.
+ *            A run's value is the sum of its group_sum (1 or 2) largest s + bias (of what there is,
+ *            where fewer can be chosen; a run without any comes last), or the largest logit where
+ *            group_sum is 1 and there is no bias.
+ *   top_k    1 .. min(E, CR_MAX_CHOICES), and at most top_groups * E / n_groups.
+ *   Ties, of runs and of experts, go to the lower index.
+ *   ids      [T, top_k] int32 out, the chosen experts from the largest key down; -1 where none is left.
+ *   weights  [T, top_k] float out: s * scale, with CR_FLAG_ROUTE_RENORM over the sum of the token's
+ *            chosen s (0 where that sum is 0); computed in FP64, rounded once; 0 beside an id of -1.
+ *   scale    finite.
+ */
+cr_status cr_route_experts(const void *logits, cr_dtype dtype, int64_t ld, int64_t T, int64_t E, const float *bias,
+                           int64_t n_groups, int64_t top_groups, int64_t group_sum, int64_t top_k, float scale,
+                           int32_t *ids, float *weights, uint32_t flags, hipStream_t stream);
+
+/*
+ * Plan: the slots of experts first .. first + E - 1, sorted by expert and, of one expert, in their
+ * order.
+ *   ids      [T, top_k] int32, in any order and with repetitions; others than the experts here are
+ *            left out.
+ *   offsets  [E + 1] int32 out: the slots of expert first + e are rows[offsets[e] .. offsets[e+1]-1].
+ *   rows     [T * top_k] int32 out; -1 in the places from offsets[E] on.
+ *   workspace   cr_experts_plan_workspace_bytes(T, top_k, E) bytes, 256-byte aligned; may be NULL where
+ *            that is 0.  Nothing in it needs to start at zero.
+ * Without tokens offsets are still written (zeros).
+ */
+size_t cr_experts_plan_workspace_bytes(int64_t T, int64_t top_k, int64_t E);
+cr_status cr_experts_plan(const int32_t *ids, int64_t T, int64_t top_k, int64_t first, int64_t E, int32_t *offsets,
+                          int32_t *rows, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The experts' products: cr_gemm_s8s4_rowscale with a weight for each run of rows.  For place i of expert e
+ * (offsets[e] <= i < offsets[e+1]):
+ *   out = ((float)sum_k a_s8[s, k] q[e, n, k] * a_scale[s]) * b_scale[e, n] (+ bias[e, n]),
+ * s = rows[i] / gather with gather > 0 (top_k: the rows of A are tokens; 1: slots), or i with gather = 0,
+ * written to row rows[i] of C with CR_FLAG_EXPERTS_SCATTER, otherwise to row i.  Each output bit is that of
+ * cr_gemm_s8s4_rowscale on the expert's rows.
+ * With CR_FLAG_EXPERTS_SWIGLU the N weight rows are N/2 gates, then their N/2 values, and C has N/2 columns:
+ * the SwiGLU element (above) of the two FP32 results, rounded once to c_dtype.
+ *   a_s8     [M, lda] int8, a_scale [M] float, as for cr_gemm_s8s4_rowscale.
+ *   b_s4     [E, N, ldb bytes] packed rows, b_stride bytes from one expert to the next (>= N * ldb, a
+ *            multiple of 16); b_scale, bias [E, N] float (bias may be NULL).
+ *   offsets, rows   as cr_experts_plan writes them for S slots (rows may be NULL without gather and
+ *            scatter).  Offsets beyond S and rows beyond M or S are not followed.
+ *   c        [S, ldc] of c_dtype, element-aligned (CR_I32: the sums, without bias and SwiGLU).  Rows that
+ *            no place names, and columns past the last, are left as they are.
+ */
+cr_status cr_gemm_s8s4_experts(const int8_t *a_s8, int64_t lda, const float *a_scale, int64_t M,
+                               const uint8_t *b_s4, int64_t ldb, int64_t b_stride, const float *b_scale,
+                               const float *bias, const int32_t *offsets, const int32_t *rows, int64_t S, int64_t E,
+                               int64_t N, int64_t K_pad, int64_t gather, void *c, cr_dtype c_dtype, int64_t ldc,
+                               uint32_t flags, hipStream_t stream);
+
+/*
+ * Weighted sum of each token's experts:
+ *   out[t] = sum_j weights[t, j] * y[t * top_k + j] (+ residual[t]),
+ * over the choices of experts first .. first + E - 1, in FP32 with fused multiply-adds from j = 0 up, the
+ * residual last, rounded once.  Rows of y of other choices are not read; a token without any gives 0, or
+ * its residual.
+ *   y [T * top_k, ld_y], residual [T, ld_res] or NULL, out [T, ld_out] of dtype (CR_BF16, CR_FP16 or
+ *   CR_FP32), N columns, element-aligned (rows of 16-byte multiples are fastest).  out may be residual,
+ *   with its row stride.
+ */
+cr_status cr_experts_combine(const void *y, cr_dtype dtype, int64_t ld_y, const float *weights, const int32_t *ids,
+                             int64_t T, int64_t top_k, int64_t first, int64_t E, int64_t N, const void *residual,
+                             int64_t ld_res, void *out, int64_t ld_out, hipStream_t stream);
+
+/*
+ * The layer: the plan, cr_gemm_s8s4_experts with SwiGLU and gather = top_k (w1 [E, 2F, K]: gates, then
+ * values), cr_quant_act of its rows (kept in dtype), cr_gemm_s8s4_experts with scatter (w2 [E, N, F]) and
+ * cr_experts_combine, bit for bit as these calls one after another, on `stream`.
+ *   a_s8 [T, lda] with K_pad columns, a_scale   the tokens' prepared rows (cr_quant_act, cr_quant_act_rmsnorm).
+ *   ids, weights   [T, top_k] as cr_route_experts writes them.
+ *   w1, w2   packed rows with their strides, scales and biases as in cr_gemm_s8s4_experts; w2's rows hold
+ *            256 * ceil(F / 256) columns.
+ *   residual, out   [T, ld] of dtype (CR_BF16, CR_FP16 or CR_FP32) as in cr_experts_combine.
+ *   workspace   cr_mlp_experts_w4a8_workspace_bytes(...) bytes, 256-byte aligned.  Nothing in it needs to
+ *            start at zero.  N is at most 2^28 (CR_ERR_TOO_LARGE beyond).
+ *   flags    CR_FLAG_BLOCK_TRANSPOSED when w2's codes are in that order, CR_FLAG_FORCE_TWO_PASS (both as
+ *            for cr_quant_act).
+ */
+size_t cr_mlp_experts_w4a8_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t F, int64_t N, cr_dtype dtype);
+cr_status cr_mlp_experts_w4a8(const int8_t *a_s8, int64_t lda, const float *a_scale, int64_t T, int64_t K_pad,
+                              const int32_t *ids, const float *weights, int64_t top_k, int64_t first, int64_t E,
+                              const uint8_t *w1, int64_t ld1, int64_t stride1, const float *scale1,
+                              const float *bias1, int64_t F, const uint8_t *w2, int64_t ld2, int64_t stride2,
+                              const float *scale2, const float *bias2, int64_t N, const void *residual,
+                              int64_t ld_res, void *out, cr_dtype dtype, int64_t ld_out, void *workspace,
+                              size_t ws_bytes, uint32_t flags, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,8 @@ CR_ABI_VERSION = 3
 CR_BF16, CR_FP16, CR_FP32, CR_I32 = 0, 1, 2, 3
 CR_FLAG_NONE, CR_FLAG_FORCE_TWO_PASS, CR_FLAG_BLOCK_TRANSPOSED = 0, 1, 2
 CR_FLAG_CAUSAL, CR_FLAG_ROPE_INTERLEAVED = 16, 32
+CR_FLAG_ROUTE_SIGMOID, CR_FLAG_ROUTE_RENORM, CR_FLAG_EXPERTS_SCATTER, CR_FLAG_EXPERTS_SWIGLU = 64, 128, 256, 512
+CR_MAX_EXPERTS, CR_MAX_CHOICES, CR_MAX_EXPERT_GROUPS = 512, 32, 64
 KV8_PAGE = 64
 CR_MAX_K_PAD = 133120
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -106,6 +108,15 @@ def lib() -> C.CDLL:
             "cr_attn_kv8_workspace_bytes": (sz, [i64, i64, i64, i64, i64, i64, i64]),
             "cr_attn_kv8": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, vp, i64, i64, i64, i64, i64, C.POINTER(_Kv8),
                                       C.c_float, vp, i64, vp, sz, u32, vp]),
+            "cr_route_experts": (C.c_int, [vp, C.c_int, i64, i64, i64, vp, i64, i64, i64, i64, C.c_float, vp, vp, u32, vp]),
+            "cr_experts_plan_workspace_bytes": (sz, [i64, i64, i64]),
+            "cr_experts_plan": (C.c_int, [vp, i64, i64, i64, i64, vp, vp, vp, sz, vp]),
+            "cr_gemm_s8s4_experts": (C.c_int, [vp, i64, vp, i64, vp, i64, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp,
+                                               C.c_int, i64, u32, vp]),
+            "cr_experts_combine": (C.c_int, [vp, C.c_int, i64, vp, vp, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp]),
+            "cr_mlp_experts_w4a8_workspace_bytes": (sz, [i64, i64, i64, i64, i64, C.c_int]),
+            "cr_mlp_experts_w4a8": (C.c_int, [vp, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, vp,
+                                              i64, i64, vp, vp, i64, vp, i64, vp, C.c_int, i64, vp, sz, u32, vp]),
             "cr_gemm_nvfp4_fused": (C.c_int, [vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, vp,
                                               C.c_int, i64, u32, vp]),
         }
@@ -522,6 +533,112 @@ def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm
         raise CrError("cr_attn_kv8", status)
 
 
+def _choices(ids, weights=None):
+    """(address of ids, T, top_k); weights, when given, must go with them."""
+    if ids.dtype is not torch.int32 or ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 tensor [T, top_k]")
+    T, k = ids.shape
+    if weights is not None and (weights.dtype is not torch.float32 or weights.shape != ids.shape
+                                or not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous float32 tensor of the shape of ids")
+    return ids.data_ptr(), T, k
+
+
+def _expert_weight(name, w, scale, bias):
+    """(address, ldb, stride, scale, bias, E, N) of a packed weight [E, N, bytes] with its scales and bias."""
+    if w.dtype is not torch.uint8 or w.dim() != 3 or (w.stride(2) != 1 and w.size(2) > 1):
+        raise ValueError(f"{name} must be a uint8 tensor [E, N, bytes] with contiguous rows")
+    E, N, _ = w.shape
+    return (w.data_ptr(), w.stride(1), w.stride(0), _vector(f"the scales of {name}", scale, E * N),
+            _vector(f"the bias of {name}", bias, E * N), E, N)
+
+
+def _out_rows(name, t, rows, cols, dtype=None):
+    """(address, row stride) of an optional [rows, cols] tensor."""
+    if t is None:
+        return None, cols
+    if t.shape != (rows, cols) or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"{name} must be [{rows}, {cols}]" + (f" of {dtype}" if dtype is not None else ""))
+    return t.data_ptr(), max(_ld(t), cols)
+
+
+def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags=0, stream=None):
+    ld = _ld(logits)
+    T, E = logits.shape
+    i, n, k = _choices(ids, weights)
+    if n != T or k != top_k:
+        raise ValueError("ids must be [T, top_k]")
+    status = lib().cr_route_experts(
+        logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), max(ld, E), T, E, _vector("bias", bias, E), n_groups,
+        top_groups, group_sum, top_k, scale, i, weights.data_ptr(), flags, _stream(stream))
+    if status:
+        raise CrError("cr_route_experts", status)
+
+
+def cr_experts_plan_workspace_bytes(T, top_k, E) -> int:
+    return int(lib().cr_experts_plan_workspace_bytes(T, top_k, E))
+
+
+def cr_experts_plan(ids, first, E, offsets, rows, workspace=None, stream=None):
+    i, T, k = _choices(ids)
+    status = lib().cr_experts_plan(
+        i, T, k, first, E, _vector("offsets", offsets, E + 1, torch.int32), _vector("rows", rows, T * k, torch.int32),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, _stream(stream))
+    if status:
+        raise CrError("cr_experts_plan", status)
+
+
+def cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, gather, c, flags=0, stream=None):
+    lda = _ld(a_s8)
+    M, K_pad = a_s8.shape
+    b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias)
+    S = rows.numel()
+    cols = N // 2 if flags & CR_FLAG_EXPERTS_SWIGLU else N
+    c_ptr, ldc = _out_rows("c", c, S, cols)
+    status = lib().cr_gemm_s8s4_experts(
+        a_s8.data_ptr(), max(lda, K_pad), _vector("a_scale", a_scale, M), M, b, ldb, stride, scale, bias,
+        _vector("offsets", offsets, E + 1, torch.int32), _vector("rows", rows, S, torch.int32), S, E, N, K_pad, gather, c_ptr,
+        _TORCH_TO_CR.get(c.dtype, -1), ldc, flags, _stream(stream))
+    if status:
+        raise CrError("cr_gemm_s8s4_experts", status)
+
+
+def cr_experts_combine(y, weights, ids, first, E, residual, out, stream=None):
+    i, T, k = _choices(ids, weights)
+    N = y.shape[1]
+    y_ptr, ld_y = _out_rows("y", y, T * k, N)
+    o, ld_out = _out_rows("out", out, T, N, y.dtype)
+    r, ld_r = _out_rows("residual", residual, T, N, y.dtype)
+    status = lib().cr_experts_combine(y_ptr, _TORCH_TO_CR.get(y.dtype, -1), ld_y, weights.data_ptr(), i, T, k, first, E, N,
+                                      r, ld_r, o, ld_out, _stream(stream))
+    if status:
+        raise CrError("cr_experts_combine", status)
+
+
+def cr_mlp_experts_w4a8_workspace_bytes(T, top_k, E, F, N, dtype) -> int:
+    return int(lib().cr_mlp_experts_w4a8_workspace_bytes(T, top_k, E, F, N, _TORCH_TO_CR.get(dtype, -1)))
+
+
+def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w2, scale2, bias2, residual, out,
+                        workspace, flags=0, stream=None):
+    i, T, k = _choices(ids, weights)
+    lda = _ld(a_s8)
+    M, K_pad = a_s8.shape
+    p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1)
+    p2, ld2, stride2, s2, b2, E2, N = _expert_weight("w2", w2, scale2, bias2)
+    if M != T or E2 != E or rows1 % 2:
+        raise ValueError("a_s8 must hold T rows, w1 an even number of rows, and w1 and w2 the same experts")
+    o, ld_out = _out_rows("out", out, T, N)
+    r, ld_r = _out_rows("residual", residual, T, N, out.dtype)
+    status = lib().cr_mlp_experts_w4a8(
+        a_s8.data_ptr(), max(lda, K_pad), _vector("a_scale", a_scale, T), T, K_pad, i, weights.data_ptr(), k, first, E, p1,
+        ld1, stride1, s1, b1, rows1 // 2, p2, ld2, stride2, s2, b2, N, r, ld_r, o, _TORCH_TO_CR.get(out.dtype, -1), ld_out,
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, flags,
+        _stream(stream))
+    if status:
+        raise CrError("cr_mlp_experts_w4a8", status)
+
+
 # ---------------------------------------------------------------- conveniences ----
 
 def quant_act(x: torch.Tensor, K: int | None = None, swiglu: bool = False, flags: int = 0,
@@ -726,4 +843,75 @@ def attn_kv8(q, cache: Kv8Cache, cu_seqlens, kv_lens, page_table, max_q: int, ma
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
     cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table,
                 cache.D ** -0.5 if sm_scale is None else sm_scale, out, workspace, CR_FLAG_CAUSAL if causal else 0)
+    return out
+
+
+def quant_experts_w4(w: torch.Tensor, flags: int = 0):
+    """(packed 4-bit codes [E, N, K_pad / 2] uint8, scales [E, N] fp32) of dense weights [E, N, K]."""
+    E, N, K = w.shape
+    rows = torch.nn.functional.pad(w, (0, -K % (16 // w.element_size())))     # rows of 16-byte multiples
+    q, s = quant_weight_w4(rows.reshape(E * N, -1), K, flags)
+    return q.view(E, N, -1), s.view(E, N)
+
+
+def route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None, n_groups: int = 1,
+                  top_groups: int | None = None, group_sum: int = 2, sigmoid: bool = False, renorm: bool = True,
+                  scale: float = 1.0):
+    """(ids [T, top_k] int32, weights [T, top_k] fp32) of the experts that each row of logits [T, E]
+    chooses, by softmax or sigmoid scores; -1 and 0 where no expert is left."""
+    T = logits.shape[0]
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
+    cr_route_experts(logits, bias, n_groups, n_groups if top_groups is None else top_groups, group_sum, top_k, scale, ids,
+                     weights, (CR_FLAG_ROUTE_SIGMOID if sigmoid else 0) | (CR_FLAG_ROUTE_RENORM if renorm else 0))
+    return ids, weights
+
+
+def experts_plan(ids: torch.Tensor, E: int, first: int = 0, workspace=None):
+    """(offsets [E + 1] int32, rows [T * top_k] int32): the slots (choice j of token t: t * top_k + j) of
+    experts first .. first + E - 1, sorted by expert; -1 behind them."""
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
+    rows = torch.empty(ids.numel(), dtype=torch.int32, device=ids.device)
+    if workspace is None and ids.dim() == 2:
+        need = cr_experts_plan_workspace_bytes(*ids.shape, E)
+        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
+    cr_experts_plan(ids, first, E, offsets, rows, workspace)
+    return offsets, rows
+
+
+def gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, offsets, rows, top_k: int, out_dtype=torch.bfloat16, bias=None,
+                      gather: bool = False, scatter: bool = False, swiglu: bool = False, out=None):
+    """The rows of each expert times its 4-bit weight b_s4 [E, N, K_pad / 2].  gather: a_s8 holds the tokens'
+    rows, otherwise the rows in the plan's order; scatter: the output is in the order of the slots, otherwise
+    in the plan's.  swiglu: N/2 columns, SwiGLU of the first half (gates) with the second."""
+    if out is None:
+        N = b_s4.shape[1]
+        out = torch.empty(rows.numel(), N // 2 if swiglu else N, dtype=out_dtype, device=a_s8.device)
+    cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, top_k if gather else 0, out,
+                         (CR_FLAG_EXPERTS_SCATTER if scatter else 0) | (CR_FLAG_EXPERTS_SWIGLU if swiglu else 0))
+    return out
+
+
+def experts_combine(y, weights, ids, E: int, first: int = 0, residual=None, out=None):
+    """sum_j weights[t, j] * y[t * top_k + j] (+ residual[t]) over the choices of experts first .. first + E - 1;
+    `out` may be residual."""
+    if out is None:
+        out = y.new_empty(ids.shape[0], y.shape[1])
+    cr_experts_combine(y, weights, ids, first, E, residual, out)
+    return out
+
+
+def mlp_experts_w4a8(a_s8, a_scale, ids, weights, w1, scale1, w2, scale2, first: int = 0, bias1=None, bias2=None,
+                     residual=None, out_dtype=torch.bfloat16, out=None, workspace=None, flags: int = 0):
+    """The layer of experts on prepared rows a_s8 [T, K_pad]: w1 [E, 2F, K_pad / 2] (gates, then values), SwiGLU,
+    w2 [E, N, F_pad / 2], and the weighted sum (+ residual) [T, N].  `out` may be residual."""
+    T, top_k = ids.shape
+    E, N = w2.shape[:2]
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=a_s8.device)
+    if workspace is None:
+        need = cr_mlp_experts_w4a8_workspace_bytes(T, top_k, E, w1.shape[1] // 2, N, out.dtype)
+        workspace = torch.empty(need, dtype=torch.uint8, device=a_s8.device) if need else None
+    cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w2, scale2, bias2, residual, out, workspace,
+                        flags)
     return out

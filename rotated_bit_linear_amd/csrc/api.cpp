@@ -399,6 +399,146 @@ bool attn_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, 
     return true;
 }
 
+// ---- a layer of experts ----
+
+static_assert(CR_MAX_EXPERTS == convrot::kMostExperts && CR_MAX_CHOICES == convrot::kMostChoices &&
+              CR_MAX_EXPERT_GROUPS == convrot::kMostGroups, "limits of the header and the kernels");
+
+// tokens, choices and the experts here
+cr_status check_slots(int64_t T, int64_t top_k, int64_t first, int64_t E)
+{
+    if (T < 0 || top_k < 1 || top_k > CR_MAX_CHOICES || E < 1 || E > CR_MAX_EXPERTS) return CR_ERR_INVALID_ARG;
+    if (first < 0 || first > kMaxRows - E || T > kMaxRows / top_k) return CR_ERR_INVALID_ARG;
+    return CR_OK;
+}
+
+bool is_float(cr_dtype d) { return d == CR_BF16 || d == CR_FP16 || d == CR_FP32; }
+
+// one weight of every expert: packed rows, strides in bytes, scales and an optional bias
+cr_status check_expert_weight(const uint8_t *w, int64_t ld, int64_t stride, const float *scale, const float *bias,
+                              int64_t N, int64_t K_pad, bool needs_scale)
+{
+    if (N > 0 && (!w || (needs_scale && !scale))) return CR_ERR_INVALID_ARG;
+    if (N < 0 || N > kMaxRows || K_pad < 1 || K_pad % 256 != 0) return CR_ERR_INVALID_ARG;
+    if (K_pad > CR_MAX_K_PAD) return CR_ERR_TOO_LARGE;
+    if (ld < K_pad / 2 || ld > kMaxRows || stride < N * ld) return CR_ERR_INVALID_ARG;
+    if (!aligned(w, 16) || ld % 16 != 0 || stride % 16 != 0 || !aligned(scale, 4) || !aligned(bias, 4))
+        return CR_ERR_MISALIGNED;
+    return CR_OK;
+}
+
+cr_status check_experts_gemm(const int8_t *a, int64_t lda, const float *sa, int64_t M, const uint8_t *b, int64_t ldb,
+                             int64_t stride, const float *sb, const float *bias, const int32_t *offsets,
+                             const int32_t *rows, int64_t S, int64_t E, int64_t N, int64_t K_pad, int64_t gather,
+                             const void *c, cr_dtype cdt, int64_t ldc, uint32_t flags)
+{
+    const bool swiglu = (flags & CR_FLAG_EXPERTS_SWIGLU) != 0, scatter = (flags & CR_FLAG_EXPERTS_SCATTER) != 0;
+    if (!is_float(cdt) && cdt != CR_I32) return CR_ERR_UNSUPPORTED_DTYPE;
+    if (flags & ~(uint32_t)(CR_FLAG_EXPERTS_SCATTER | CR_FLAG_EXPERTS_SWIGLU)) return CR_ERR_INVALID_ARG;
+    if (M < 0 || S < 0 || M > kMaxRows || S > kMaxRows || E < 1 || E > CR_MAX_EXPERTS) return CR_ERR_INVALID_ARG;
+    if (gather < 0 || gather > CR_MAX_CHOICES) return CR_ERR_INVALID_ARG;
+    if (cdt == CR_I32 && (swiglu || bias)) return CR_ERR_INVALID_ARG;
+    if (swiglu && N % 2 != 0) return CR_ERR_INVALID_ARG;
+    const bool any = S > 0 && N > 0 && M > 0;
+    cr_status s = check_expert_weight(b, ldb, stride, sb, bias, N, K_pad, cdt != CR_I32);
+    if (s != CR_OK) return s;
+    if (lda < K_pad || ldc < (swiglu ? N / 2 : N)) return CR_ERR_INVALID_ARG;
+    if (any && (!a || !offsets || !c || (cdt != CR_I32 && !sa))) return CR_ERR_INVALID_ARG;
+    if (any && (gather > 0 || scatter) && !rows) return CR_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || lda % 16 != 0 || !aligned(sa, 4) || !aligned(offsets, 4) || !aligned(rows, 4))
+        return CR_ERR_MISALIGNED;
+    if (!aligned(c, (size_t)elem_size(cdt))) return CR_ERR_MISALIGNED;
+    // 32-bit count of work-items
+    if (any && convrot::experts_gemm_blocks(S, E, N, swiglu) > convrot::kMostBlocks) return CR_ERR_TOO_LARGE;
+    return CR_OK;
+}
+
+cr_status check_combine(const void *y, cr_dtype dt, int64_t ld_y, const float *weights, const int32_t *ids, int64_t T,
+                        int64_t top_k, int64_t first, int64_t E, int64_t N, const void *residual, int64_t ld_res,
+                        const void *out, int64_t ld_out)
+{
+    if (!is_float(dt)) return CR_ERR_UNSUPPORTED_DTYPE;
+    cr_status s = check_slots(T, top_k, first, E);
+    if (s != CR_OK) return s;
+    if (N < 0 || N > kMaxRows || ld_y < N || ld_out < N || (residual && ld_res < N)) return CR_ERR_INVALID_ARG;
+    if (T > 0 && N > 0 && (!y || !weights || !ids || !out)) return CR_ERR_INVALID_ARG;
+    if (residual && residual == out && ld_res != ld_out) return CR_ERR_INVALID_ARG;
+    const size_t es = (size_t)elem_size(dt);
+    if (!aligned(y, es) || !aligned(residual, es) || !aligned(out, es) || !aligned(weights, 4) || !aligned(ids, 4))
+        return CR_ERR_MISALIGNED;
+    // workgroups of 256 threads with at least one column each
+    if (T > 0 && (N + 255) / 256 > convrot::kMostBlocks / T) return CR_ERR_TOO_LARGE;
+    return CR_OK;
+}
+
+size_t plan_bytes(int64_t S, int64_t E)
+{
+    int64_t runs, run;
+    convrot::plan_runs(S, runs, run);
+    return runs > 1 ? up256((size_t)runs * (size_t)(E + 1) * 4) : 0;
+}
+
+convrot::PlanLaunch plan_launch(const int32_t *ids, int64_t S, int64_t first, int64_t E, int32_t *offsets, int32_t *rows,
+                                void *workspace)
+{
+    convrot::PlanLaunch p{};
+    p.ids = ids; p.S = S; p.first = (int)first; p.E = (int)E; p.offsets = offsets; p.rows = rows;
+    p.counts = static_cast<int32_t *>(workspace);
+    return p;
+}
+
+convrot::ExpertsGemm experts_gemm(const int8_t *a, int64_t lda, const float *sa, int64_t M, const uint8_t *b, int64_t ldb,
+                                  int64_t stride, const float *sb, const float *bias, const int32_t *offsets,
+                                  const int32_t *rows, int64_t S, int64_t E, int64_t N, int64_t K_pad, int64_t gather,
+                                  bool scatter, void *c, int64_t ldc)
+{
+    convrot::ExpertsGemm g{};
+    g.A = a; g.lda = lda; g.sa = sa; g.M = (int)M; g.B = b; g.ldb = ldb; g.stride_b = stride; g.sb = sb; g.bias = bias;
+    g.offsets = offsets; g.rows = rows; g.S = (int)S; g.E = (int)E; g.N = (int)N; g.K_pad = (int)K_pad;
+    g.gather = (int)gather; g.scatter = scatter; g.C = c; g.ldc = ldc;
+    return g;
+}
+
+convrot::CombineLaunch combine_launch(const void *y, int64_t ld_y, const float *weights, const int32_t *ids, int64_t T,
+                                      int64_t top_k, int64_t first, int64_t E, int64_t N, const void *residual,
+                                      int64_t ld_res, void *out, int64_t ld_out)
+{
+    convrot::CombineLaunch c{};
+    c.y = y; c.ld_y = ld_y; c.weights = weights; c.ids = ids; c.T = T; c.k = (int)top_k; c.first = (int)first;
+    c.E = (int)E; c.N = (int)N; c.residual = residual; c.ld_res = ld_res; c.out = out; c.ld_out = ld_out;
+    return c;
+}
+
+constexpr int64_t kMostExpertCols = 1 << 28;     // columns of the layer's output: byte counts stay below 2^63
+
+// Workspace of the layer of experts (every region 256-byte aligned): the plan, the rows between the
+// products [S, ld_h], their codes and scales, the experts' rows [S, ld_y].
+struct ExpertsPlan {
+    int64_t S, F_pad, ld_h, ld_y;
+    size_t off_offsets, off_rows, off_counts, off_h, off_q, off_scale, off_y, bytes;
+};
+
+ExpertsPlan plan_experts_layer(int64_t T, int64_t top_k, int64_t E, int64_t F, int64_t N, cr_dtype dt)
+{
+    ExpertsPlan p{};
+    const int64_t es = elem_size(dt), row = 16 / es;
+    p.S = T * top_k;
+    p.F_pad = pad256(F);
+    p.ld_h = (F + row - 1) / row * row;
+    p.ld_y = (N + row - 1) / row * row;
+    size_t at = 0;
+    auto region = [&](size_t bytes) { const size_t o = at; at += up256(bytes); return o; };
+    p.off_offsets = region((size_t)(E + 1) * 4);
+    p.off_rows = region((size_t)p.S * 4);
+    p.off_counts = region(plan_bytes(p.S, E));
+    p.off_h = region((size_t)p.S * (size_t)p.ld_h * (size_t)es);
+    p.off_q = region((size_t)p.S * (size_t)p.F_pad);
+    p.off_scale = region((size_t)p.S * 4);
+    p.off_y = region((size_t)p.S * (size_t)p.ld_y * (size_t)es);
+    p.bytes = at;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1106,6 +1246,148 @@ cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, in
     l.cache = kv8_ptrs(cache); l.sm_scale = sm_scale; l.causal = (flags & CR_FLAG_CAUSAL) != 0;
     l.workspace = workspace; l.plan = p;
     return from_hip(convrot::launch_attn_kv8(l, stream));
+}
+
+cr_status cr_route_experts(const void *logits, cr_dtype dtype, int64_t ld, int64_t T, int64_t E, const float *bias,
+                           int64_t n_groups, int64_t top_groups, int64_t group_sum, int64_t top_k, float scale,
+                           int32_t *ids, float *weights, uint32_t flags, hipStream_t stream)
+{
+    if (!is_float(dtype)) return CR_ERR_UNSUPPORTED_DTYPE;
+    if (flags & ~(uint32_t)(CR_FLAG_ROUTE_SIGMOID | CR_FLAG_ROUTE_RENORM)) return CR_ERR_INVALID_ARG;
+    cr_status s = check_slots(T, top_k, 0, E);
+    if (s != CR_OK) return s;
+    if (T > 0 && (!logits || !ids || !weights)) return CR_ERR_INVALID_ARG;
+    if (ld < E || group_sum < 1 || group_sum > 2) return CR_ERR_INVALID_ARG;
+    if (n_groups < 1 || n_groups > CR_MAX_EXPERT_GROUPS || E % n_groups != 0) return CR_ERR_INVALID_ARG;
+    if (top_groups < 1 || top_groups > n_groups || top_k > top_groups * (E / n_groups)) return CR_ERR_INVALID_ARG;
+    if (!(scale >= -3.402823466e38f && scale <= 3.402823466e38f)) return CR_ERR_INVALID_ARG;
+    if (!aligned(logits, (size_t)elem_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+        return CR_ERR_MISALIGNED;
+    if (T == 0) return CR_OK;
+    if (T > convrot::kMostBlocks) return CR_ERR_TOO_LARGE;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    convrot::RouteLaunch r{};
+    r.logits = logits; r.ld = ld; r.T = T; r.E = (int)E; r.G = (int)n_groups; r.top_groups = (int)top_groups;
+    r.group_sum = (int)group_sum; r.k = (int)top_k; r.bias = bias; r.scale = scale;
+    r.sigmoid = (flags & CR_FLAG_ROUTE_SIGMOID) != 0; r.renorm = (flags & CR_FLAG_ROUTE_RENORM) != 0;
+    r.ids = ids; r.weights = weights;
+    return from_hip(convrot::launch_route_experts(r, (int)dtype, stream));
+}
+
+size_t cr_experts_plan_workspace_bytes(int64_t T, int64_t top_k, int64_t E)
+{
+    return check_slots(T, top_k, 0, E) == CR_OK && T > 0 ? plan_bytes(T * top_k, E) : 0;
+}
+
+cr_status cr_experts_plan(const int32_t *ids, int64_t T, int64_t top_k, int64_t first, int64_t E, int32_t *offsets,
+                          int32_t *rows, void *workspace, size_t ws_bytes, hipStream_t stream)
+{
+    cr_status s = check_slots(T, top_k, first, E);
+    if (s != CR_OK) return s;
+    if (!offsets || (T > 0 && (!ids || !rows))) return CR_ERR_INVALID_ARG;
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(rows, 4)) return CR_ERR_MISALIGNED;
+    const size_t need = T > 0 ? plan_bytes(T * top_k, E) : 0;
+    if (need > 0) {
+        if (!workspace) return CR_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return CR_ERR_MISALIGNED;
+        if (ws_bytes < need) return CR_ERR_TOO_LARGE;
+    }
+    if ((s = current_device_ok()) != CR_OK) return s;
+    return from_hip(convrot::launch_experts_plan(plan_launch(ids, T * top_k, first, E, offsets, rows, workspace), stream));
+}
+
+cr_status cr_gemm_s8s4_experts(const int8_t *a_s8, int64_t lda, const float *a_scale, int64_t M,
+                               const uint8_t *b_s4, int64_t ldb, int64_t b_stride, const float *b_scale,
+                               const float *bias, const int32_t *offsets, const int32_t *rows, int64_t S, int64_t E,
+                               int64_t N, int64_t K_pad, int64_t gather, void *c, cr_dtype c_dtype, int64_t ldc,
+                               uint32_t flags, hipStream_t stream)
+{
+    cr_status s = check_experts_gemm(a_s8, lda, a_scale, M, b_s4, ldb, b_stride, b_scale, bias, offsets, rows, S, E, N,
+                                     K_pad, gather, c, c_dtype, ldc, flags);
+    if (s != CR_OK || S == 0 || N == 0 || M == 0) return s;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    return from_hip(convrot::launch_gemm_experts(
+        experts_gemm(a_s8, lda, a_scale, M, b_s4, ldb, b_stride, b_scale, bias, offsets, rows, S, E, N, K_pad, gather,
+                     (flags & CR_FLAG_EXPERTS_SCATTER) != 0, c, ldc),
+        (int)c_dtype, (flags & CR_FLAG_EXPERTS_SWIGLU) != 0, stream));
+}
+
+cr_status cr_experts_combine(const void *y, cr_dtype dtype, int64_t ld_y, const float *weights, const int32_t *ids,
+                             int64_t T, int64_t top_k, int64_t first, int64_t E, int64_t N, const void *residual,
+                             int64_t ld_res, void *out, int64_t ld_out, hipStream_t stream)
+{
+    cr_status s = check_combine(y, dtype, ld_y, weights, ids, T, top_k, first, E, N, residual, ld_res, out, ld_out);
+    if (s != CR_OK || T == 0 || N == 0) return s;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    return from_hip(convrot::launch_experts_combine(
+        combine_launch(y, ld_y, weights, ids, T, top_k, first, E, N, residual, ld_res, out, ld_out), (int)dtype, stream));
+}
+
+size_t cr_mlp_experts_w4a8_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t F, int64_t N, cr_dtype dtype)
+{
+    if (check_slots(T, top_k, 0, E) != CR_OK || T < 1 || F < 1 || N < 1 || N > kMostExpertCols || !is_float(dtype) ||
+        F > CR_MAX_K_PAD || pad256(F) > CR_MAX_K_PAD)
+        return 0;
+    return plan_experts_layer(T, top_k, E, F, N, dtype).bytes;
+}
+
+cr_status cr_mlp_experts_w4a8(const int8_t *a_s8, int64_t lda, const float *a_scale, int64_t T, int64_t K_pad,
+                              const int32_t *ids, const float *weights, int64_t top_k, int64_t first, int64_t E,
+                              const uint8_t *w1, int64_t ld1, int64_t stride1, const float *scale1,
+                              const float *bias1, int64_t F, const uint8_t *w2, int64_t ld2, int64_t stride2,
+                              const float *scale2, const float *bias2, int64_t N, const void *residual,
+                              int64_t ld_res, void *out, cr_dtype dtype, int64_t ld_out, void *workspace,
+                              size_t ws_bytes, uint32_t flags, hipStream_t stream)
+{
+    if (!is_float(dtype)) return CR_ERR_UNSUPPORTED_DTYPE;
+    cr_status s = check_slots(T, top_k, first, E);
+    if (s != CR_OK) return s;
+    if (check_flags(flags) != CR_OK || F < 1 || N < 0) return CR_ERR_INVALID_ARG;
+    if (F > CR_MAX_K_PAD || pad256(F) > CR_MAX_K_PAD || N > kMostExpertCols) return CR_ERR_TOO_LARGE;
+    const ExpertsPlan p = plan_experts_layer(T, top_k, E, F, N, dtype);
+    const bool any = T > 0 && N > 0;
+    // addresses of the workspace, or (an empty layer: nothing is enqueued) none
+    int8_t *const ws = static_cast<int8_t *>(any ? workspace : nullptr);
+    if (any) {
+        if (!workspace) return CR_ERR_INVALID_ARG;
+        if (!aligned(workspace, 256)) return CR_ERR_MISALIGNED;
+        if (ws_bytes < p.bytes) return CR_ERR_TOO_LARGE;
+        if (!ids) return CR_ERR_INVALID_ARG;
+    }
+    auto at = [&](size_t off) { return any ? ws + off : nullptr; };
+    int32_t *offsets = reinterpret_cast<int32_t *>(at(p.off_offsets));
+    int32_t *rows = reinterpret_cast<int32_t *>(at(p.off_rows));
+    void *h = at(p.off_h), *y = at(p.off_y);
+    int8_t *q = at(p.off_q);
+    float *q_scale = reinterpret_cast<float *>(at(p.off_scale));
+    // validate every call before enqueueing anything; without columns the first product is checked too
+    const int64_t S = any ? p.S : 0;
+    s = check_experts_gemm(a_s8, lda, a_scale, T, w1, ld1, stride1, scale1, bias1, offsets, rows, S, E, 2 * F, K_pad,
+                           top_k, h, dtype, p.ld_h, CR_FLAG_EXPERTS_SWIGLU);
+    if (s != CR_OK) return s;
+    s = check_act(h, dtype, p.ld_h, S, F, F, q, p.F_pad, q_scale, flags);
+    if (s != CR_OK) return s;
+    s = check_experts_gemm(q, p.F_pad, q_scale, S, w2, ld2, stride2, scale2, bias2, offsets, rows, S, E, N, p.F_pad, 0, y,
+                           dtype, p.ld_y, CR_FLAG_EXPERTS_SCATTER);
+    if (s != CR_OK) return s;
+    s = check_combine(y, dtype, p.ld_y, weights, ids, any ? T : 0, top_k, first, E, N, residual, ld_res, out, ld_out);
+    if (s != CR_OK || !any) return s;
+    if ((s = current_device_ok()) != CR_OK) return s;
+    const bool tp = (flags & CR_FLAG_FORCE_TWO_PASS) != 0, tr = (flags & CR_FLAG_BLOCK_TRANSPOSED) != 0;
+    if (convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) != hipSuccess)
+        return CR_ERR_LAUNCH;
+    if (convrot::launch_gemm_experts(experts_gemm(a_s8, lda, a_scale, T, w1, ld1, stride1, scale1, bias1, offsets, rows, S,
+                                                  E, 2 * F, K_pad, top_k, false, h, p.ld_h),
+                                     (int)dtype, true, stream) != hipSuccess)
+        return CR_ERR_LAUNCH;
+    if (convrot::launch_quant_act(h, (int)dtype, p.ld_h, S, F, nullptr, q, p.F_pad, q_scale, tp, tr, stream) != hipSuccess)
+        return CR_ERR_LAUNCH;
+    if (convrot::launch_gemm_experts(experts_gemm(q, p.F_pad, q_scale, S, w2, ld2, stride2, scale2, bias2, offsets, rows, S,
+                                                  E, N, p.F_pad, 0, true, y, p.ld_y),
+                                     (int)dtype, false, stream) != hipSuccess)
+        return CR_ERR_LAUNCH;
+    return from_hip(convrot::launch_experts_combine(
+        combine_launch(y, p.ld_y, weights, ids, T, top_k, first, E, N, residual, ld_res, out, ld_out), (int)dtype, stream));
 }
 
 }  // extern "C"

@@ -153,4 +153,66 @@ struct AttnLaunch {
 };
 hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st);
 
+// ---- a layer of experts (experts.hpp) ----
+constexpr int kMostExperts = 512, kMostChoices = 32, kMostGroups = 64;
+
+struct RouteLaunch {
+    const void *logits;
+    int64_t ld, T;
+    int E, G, top_groups, group_sum, k;
+    const float *bias;
+    float scale;
+    int sigmoid, renorm;
+    int32_t *ids;
+    float *weights;
+    int lanes_lg;            // set by the launcher: log2 of the lanes that share a group
+};
+hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st);
+
+struct PlanLaunch {
+    const int32_t *ids;
+    int64_t S;
+    int first, E;
+    int32_t *offsets, *rows;
+    int32_t *counts;         // workspace [runs][E + 1], used with more than one run
+    int64_t runs, run;       // set by the launcher: runs of `run` slots
+    int bin_bits;
+};
+void plan_runs(int64_t S, int64_t &runs, int64_t &run);
+hipError_t launch_experts_plan(PlanLaunch a, hipStream_t st);
+
+struct ExpertsGemm {
+    const int8_t *A;
+    int64_t lda;
+    const float *sa;
+    int M;                   // rows of A
+    const uint8_t *B;
+    int64_t ldb, stride_b;   // bytes a weight row, bytes an expert
+    const float *sb, *bias;  // [E, N]
+    const int32_t *offsets, *rows;
+    int S, E, N, K_pad;
+    int gather;              // 0: place i reads row i; otherwise row rows[i] / gather
+    int scatter;             // place i writes row rows[i], not i
+    void *C;
+    int64_t ldc;
+    int n_tiles, vec;        // set by the launcher
+};
+// workgroups of the launch
+int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N, bool swiglu);
+hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);
+
+struct CombineLaunch {
+    const void *y;
+    int64_t ld_y, T;
+    int k, N, first, E;
+    const float *weights;
+    const int32_t *ids;
+    const void *residual;
+    int64_t ld_res;
+    void *out;
+    int64_t ld_out;
+    int pieces;              // set by the launcher: workgroups a token
+};
+hipError_t launch_experts_combine(const CombineLaunch &a, int dtype, hipStream_t st);
+
 }  // namespace convrot
