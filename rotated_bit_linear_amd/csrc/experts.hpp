@@ -45,6 +45,15 @@ __host__ __device__ inline int row_to(const ExpertsGemm &g, int i)
     return r >= 0 && r < g.S ? r : -1;
 }
 
+// blocks of all experts, found by each wave
+__device__ __forceinline__ int count_blocks(const int32_t *offsets, int E, int S, int lg, int lane)
+{
+    int n = 0;
+    for (int c = lane; c < E; c += 64)
+        n += expert_blocks(expert_offset(offsets, c, S), expert_offset(offsets, c + 1, S), lg);
+    return __builtin_amdgcn_readlane(wave_scan(n), 63);
+}
+
 // Block b of the experts' rows: block counts follow from the offsets, which only the device knows, so
 // every wave finds its own.  False where there are fewer blocks.  Whatever the offsets hold,
 // 0 <= row < end <= S.

@@ -70,7 +70,7 @@ void experts_few_kernel(const ExpertsGemm g)
     __shared__ v4i sums[kWaves][2 * MT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, q = lane >> 4;
-    constexpr int LG = MT == 1 ? 4 : MT == 2 ? 5 : 6;
+    constexpr int LG = MT == 1 ? 4 : 5;
     ExpertBlock blk;
     if (!find_block(g.offsets, g.E, g.S, LG, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
     const int half = SWIGLU ? g.N >> 1 : 0;
@@ -173,22 +173,26 @@ hipError_t launch_few(const ExpertsGemm &g, int mt, int64_t blocks, hipStream_t 
 {
     const dim3 grid((unsigned)(blocks * g.n_tiles)), threads(64 * kWaves);
     if (mt == 1) hipLaunchKernelGGL((experts_few_kernel<OUT, 1, SWIGLU>), grid, threads, 0, st, g);
-    else if (mt == 2) hipLaunchKernelGGL((experts_few_kernel<OUT, 2, SWIGLU>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((experts_few_kernel<OUT, 4, SWIGLU>), grid, threads, 0, st, g);
+    else hipLaunchKernelGGL((experts_few_kernel<OUT, 2, SWIGLU>), grid, threads, 0, st, g);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N, bool swiglu)
+// Many rows an expert on average: tiles through LDS.
+static bool tiled(int64_t S, int64_t E) { return S > 32 * E; }
+static int lg_rows(int64_t S, int64_t E) { return S <= 16 * E ? 4 : 5; }
+
+int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N, bool)
 {
-    const int lg = S <= 16 * E ? 4 : S <= 32 * E ? 5 : 6;
-    return most_blocks(S, E, lg) * ((N + kTileN - 1) / kTileN);
+    if (tiled(S, E)) return 2 * experts_tile_blocks(S, E, N);
+    return most_blocks(S, E, lg_rows(S, E)) * ((N + kTileN - 1) / kTileN);
 }
 
 hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st)
 {
-    const int lg = (int64_t)g.S <= 16 * (int64_t)g.E ? 4 : (int64_t)g.S <= 32 * (int64_t)g.E ? 5 : 6;
+    if (tiled(g.S, g.E)) return launch_experts_tile(g, out_dtype, swiglu, st);
+    const int lg = lg_rows(g.S, g.E);
     g.n_tiles = (g.N + kTileN - 1) / kTileN;
     const int es = out_dtype < 2 ? 2 : 4;
     g.vec = (uintptr_t)g.C % (4 * es) == 0 && g.ldc % 4 == 0;

@@ -72,7 +72,7 @@ class Case:
 
 
 SIZES = [(1, 1, 1, 1, 1), (1, 8, 64, 96, 512), (2, 3, 5, 33, 300), (17, 2, 4, 130, 1000), (64, 4, 16, 64, 256),
-         (40, 6, 7, 47, 2900), (300, 2, 3, 272, 520), (1000, 1, 2, 300, 256), (700, 4, 8, 516, 768), (90, 32, 40, 20, 257)]
+         (40, 6, 7, 47, 2900), (300, 2, 3, 272, 520), (1000, 1, 2, 300, 256), (700, 4, 8, 516, 768), (90, 32, 40, 20, 257), (2100, 4, 16, 1030, 512), (515, 1, 1, 4200, 256), (77, 8, 8, 768, 1280)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K", SIZES)
