@@ -449,7 +449,7 @@ cr_status check_experts_gemm(const int8_t *a, int64_t lda, const float *sa, int6
         return CR_ERR_MISALIGNED;
     if (!aligned(c, (size_t)elem_size(cdt))) return CR_ERR_MISALIGNED;
     // 32-bit count of work-items
-    if (any && convrot::experts_gemm_blocks(S, E, N, swiglu) > convrot::kMostBlocks) return CR_ERR_TOO_LARGE;
+    if (any && convrot::experts_gemm_blocks(S, E, N) > convrot::kMostBlocks) return CR_ERR_TOO_LARGE;
     return CR_OK;
 }
 

@@ -33,17 +33,18 @@ __host__ __device__ inline int expert_offset(const int32_t *offsets, int i, int 
 __host__ __device__ inline int expert_blocks(int lo, int hi, int lg) { return hi > lo ? (int)(((int64_t)hi - lo + (1 << lg) - 1) >> lg) : 0; }
 __host__ __device__ inline int block_place(int lo, int i, int lg) { return lo + (i << lg); }
 
-// row of A and row of C of a place, -1 where the plan names none
-__host__ __device__ inline int row_from(const ExpertsGemm &g, int i)
+// row of A and row of C of a place, -1 where the plan names none; `named` is rows[i], where there are rows
+__host__ __device__ inline int row_from(const ExpertsGemm &g, int i, int named)
 {
-    const int r = g.gather ? (int)((uint32_t)g.rows[i] / (uint32_t)g.gather) : i;
+    const int r = g.gather ? (int)((uint32_t)named / (uint32_t)g.gather) : i;
     return r >= 0 && r < g.M ? r : -1;
 }
-__host__ __device__ inline int row_to(const ExpertsGemm &g, int i)
+__host__ __device__ inline int row_to(const ExpertsGemm &g, int i, int named)
 {
-    const int r = g.scatter ? g.rows[i] : i;
+    const int r = g.scatter ? named : i;
     return r >= 0 && r < g.S ? r : -1;
 }
+__host__ __device__ inline int named_row(const ExpertsGemm &g, int i) { return g.gather || g.scatter ? g.rows[i] : 0; }
 
 // blocks of all experts, found by each wave
 __device__ __forceinline__ int count_blocks(const int32_t *offsets, int E, int S, int lg, int lane)
@@ -59,6 +60,7 @@ __device__ __forceinline__ int count_blocks(const int32_t *offsets, int E, int S
 // 0 <= row < end <= S.
 struct ExpertBlock {
     int e, row, end;         // expert, the block's first place in the order, and the end of the expert's
+    int blocks;              // blocks of the expert
 };
 __device__ __forceinline__ bool find_block(const int32_t *offsets, int E, int S, int lg, int b, int lane,
                                            ExpertBlock &out)
@@ -74,7 +76,8 @@ __device__ __forceinline__ bool find_block(const int32_t *offsets, int E, int S,
             const int l = __builtin_ctzll(past);
             out.e = c + l;
             out.end = __builtin_amdgcn_readlane(hi, l);
-            const int first = __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l);
+            out.blocks = __builtin_amdgcn_readlane(n, l);
+            const int first = __builtin_amdgcn_readlane(upto, l) - out.blocks;
             out.row = block_place(__builtin_amdgcn_readlane(lo, l), b - first, lg);
             return true;
         }

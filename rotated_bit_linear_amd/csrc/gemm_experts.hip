@@ -8,14 +8,17 @@
 #include <hip/hip_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "experts.hpp"
+#include "gemm_common.hpp"
 #include "kernels.hpp"
 #include "swiglu.hpp"
 
 namespace convrot {
 namespace {
 
-typedef int32_t v4i __attribute__((ext_vector_type(4)));
+using gemm::v4i;
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ v4i widen(uint32_t d0, uint32_t d1)
@@ -56,102 +59,235 @@ __device__ __forceinline__ void store4(void *C, int64_t at, const v4f &v, const 
     }
 }
 
-// A workgroup takes 16 MT rows of an expert and 32 weight rows (with SwiGLU 16 gates and their 16
-// values); its four waves share out K, each in whole lines of the weight, and add their sums in LDS.
-// Both operands go straight to registers in the order of the matrix instruction (16 x 16 x 64, weight
-// first): quarter q of a wave's lanes takes bytes 16 q of 64 of a packed row, two groups of 16 codes, one
-// for each of two instructions, and the activation's bytes of the same columns.
-constexpr int kWaves = 4, kTileN = 32;
+// A workgroup takes up to 64 rows of an expert and 128 weight rows, 32 a wave (with SwiGLU 16 gates and
+// their 16 values), and walks K in steps of 256 codes: whole lines of the weight.  Loaded to registers in the
+// order of the matrix instruction, neighbouring lanes would take 16 bytes of different rows, which the
+// texture unit works off a lane's line at a time; so both operands go to LDS by direct loads in which eight
+// (weight) and sixteen (activation) lanes share a row.  A wave's weight rows are its own, the activation's
+// are shared: one barrier a step.  The ring's 80 KB let two workgroups run on a compute unit; how many
+// steps fit follows from the rows that there are: 4 steps for up to 16 rows, 3 for 32, 2 for 64.
+constexpr int kWaves = 4, kTileN = 32 * kWaves, kLgRows = 6;
+constexpr int kStepW = kTileN * 128;                  // LDS bytes of a step's weight rows
+constexpr int kRing = 80 * 1024;
 
-template <int OUT, int MT, bool SWIGLU>
-__global__ __launch_bounds__(64 * kWaves)
-void experts_few_kernel(const ExpertsGemm g)
+__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3 & 1)) & 7; }
+
+template <int N>
+__device__ __forceinline__ void wait_vm() { __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm(N)); }
+
+// until `steps` steps of P direct loads are left in flight, at most MOST
+template <int P, int MOST, int J = 0>
+__device__ __forceinline__ void wait_steps(int steps)
 {
-    __shared__ v4i sums[kWaves][2 * MT][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (J == MOST) wait_vm<J * P>();
+    else if (steps == J) wait_vm<J * P>();
+    else wait_steps<P, MOST, J + 1>(steps);
+}
+// until step k of the prologue's D - 1 is done: behind it are the prologue's later activation loads (RM a
+// step), and k steps
+template <int RM, int D, int J = 0>
+__device__ __forceinline__ void wait_first(int k)
+{
+    constexpr int N = (D - 2 - J) * RM + J * (4 + RM);
+    if constexpr (J == D - 2) wait_vm<N>();
+    else if (k == J) wait_vm<N>();
+    else wait_first<RM, D, J + 1>(k);
+}
+
+// steps k .. of a ring, one stage after another
+template <int D, int S = 0, class Step>
+__device__ __forceinline__ void run_ring(Step &step, int &k, int nk)
+{
+    if constexpr (S < D) {
+        if (k >= nk) return;
+        step(std::integral_constant<int, S>{}, k++);
+        run_ring<D, S + 1>(step, k, nk);
+    }
+}
+
+// The products of 16 RM rows over a ring of D steps.  wsrc: the lane's source of each of the wave's four
+// direct loads of a step; a_src(j): of its load j of the activation.  once: nobody else reads these weight
+// rows, so they go past the caches (64 tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an
+// expert has several blocks its weights come from the cache the next time (777 tokens on 60: 31 us, not 36).
+template <int RM, int D, class Source, class Request>
+__device__ __forceinline__ void stream_products(int8_t *pool, const int8_t *(&wsrc)[4], Source a_src, Request request,
+                                                bool once, int nk, int wave, int lane, v4i (&acc)[2][4])
+{
+    constexpr int STEP = kStepW + RM * 4096, P = 4 + RM;     // LDS bytes, and direct loads a wave, of a step
+    static_assert(D * STEP <= kRing && D >= 2, "ring");
     const int col = lane & 15, q = lane >> 4;
-    constexpr int LG = MT == 1 ? 4 : 5;
-    ExpertBlock blk;
-    if (!find_block(g.offsets, g.E, g.S, LG, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
-    const int half = SWIGLU ? g.N >> 1 : 0;
-    const int n0 = (int)(blockIdx.x % g.n_tiles) * (SWIGLU ? kTileN / 2 : kTileN);
-    const int n_end = SWIGLU ? half : g.N;
+    auto issue_w = [&](int s, int k) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int8_t *src = wsrc[j] + (int64_t)k * 128;
+            int8_t *dst = pool + s * STEP + wave * 4096 + j * 1024;
+            if (once) __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 2);     // non-temporal
+            else __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < D - 1; s++)
+        if (s < nk) issue_w(s, s);
+    const int8_t *asrc[4];
+#pragma unroll
+    for (int j = 0; j < RM; j++) asrc[j] = a_src(j);
+    auto issue_a = [&](int s, int k) {
+#pragma unroll
+        for (int j = 0; j < RM; j++)
+            __builtin_amdgcn_global_load_lds(asrc[j] + (int64_t)k * 256,
+                                             pool + s * STEP + kStepW + j * 4096 + wave * 1024, 16, 0, 0);
+    };
+#pragma unroll
+    for (int s = 0; s < D - 1; s++)
+        if (s < nk) issue_a(s, s);
+    request();
 
-    const uint8_t *wp[2];
+    // LDS addresses of stage 0: weight chunk 4 t + q of row 16 f + col; activation chunk 8 t + 4 (q / 2) +
+    // q % 2 + 2 h of row 16 m + col (h: which of a chunk's two groups of codes)
+    const uint32_t base = (uint32_t)(uintptr_t)pool;
+    uint32_t adr_w[2], adr_a[2][2];
 #pragma unroll
-    for (int f = 0; f < 2; f++) {
-        const int n = min(n0 + (SWIGLU ? 0 : 16 * f) + col, n_end - 1) + (SWIGLU && f ? half : 0);
-        wp[f] = g.B + (int64_t)blk.e * g.stride_b + (int64_t)n * g.ldb + 16 * q;
+    for (int t = 0; t < 2; t++) {
+        adr_w[t] = base + wave * 4096 + col * 128 + (((4 * t + q) ^ swz(col)) << 4);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+            adr_a[t][h] = base + kStepW + col * 256 + (((8 * t + 4 * (q >> 1) + (q & 1) + 2 * h) ^ swz(col)) << 4);
     }
-    const int8_t *ap[MT];
+    auto lds = [](uint32_t a) { return *reinterpret_cast<const __attribute__((address_space(3))) v4i *>(a); };
+    struct Half { v4i w[2], a[4][2]; };
+    auto read = [&](Half &x, int s, int t) {
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-        const int i = blk.row + 16 * m + col;
-        const int r = i < blk.end ? row_from(g, i) : -1;
-        ap[m] = g.A + (int64_t)max(r, 0) * g.lda + 64 * (q >> 1) + 16 * (q & 1);
-    }
-    v4i acc[2][MT];
+        for (int f = 0; f < 2; f++) x.w[f] = lds(adr_w[t] + s * STEP + f * 2048);
 #pragma unroll
-    for (int f = 0; f < 2; f++)
+        for (int m = 0; m < RM; m++)
 #pragma unroll
-        for (int m = 0; m < MT; m++) acc[f][m] = v4i{0, 0, 0, 0};
-
-    for (int kb = wave; kb < g.K_pad / 256; kb += kWaves) {
-        v4i w[2][2], a[MT][4];
+            for (int h = 0; h < 2; h++) x.a[m][h] = lds(adr_a[t][h] + s * STEP + m * 4096);
+    };
+    auto multiply = [&](const Half &x) {
 #pragma unroll
-        for (int f = 0; f < 2; f++)
-#pragma unroll
-            for (int s = 0; s < 2; s++) w[f][s] = *reinterpret_cast<const v4i *>(wp[f] + kb * 128 + s * 64);
-#pragma unroll
-        for (int m = 0; m < MT; m++)
-#pragma unroll
-            for (int s = 0; s < 4; s++)
-                a[m][s] = *reinterpret_cast<const v4i *>(ap[m] + (int64_t)kb * 256 + (s >> 1) * 128 + (s & 1) * 32);
-#pragma unroll
-        for (int s = 0; s < 4; s++)
+        for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int f = 0; f < 2; f++) {
-                const v4i wide = widen((uint32_t)w[f][s >> 1][2 * (s & 1)], (uint32_t)w[f][s >> 1][2 * (s & 1) + 1]);
+                const v4i wide = widen((uint32_t)x.w[f][2 * h], (uint32_t)x.w[f][2 * h + 1]);
 #pragma unroll
-                for (int m = 0; m < MT; m++)
-                    acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wide, a[m][s], acc[f][m], 0, 0, 0);
+                for (int m = 0; m < RM; m++)
+                    acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wide, x.a[m][h], acc[f][m], 0, 0, 0);
             }
+    };
+    const bool exact_waits = nk >= 2 * (D - 1);
+    auto step = [&](auto S_, int k) {
+        constexpr int S = decltype(S_)::value;
+        // step k's loads are done: this wave's, and behind the barrier all; and all have read step k - 1
+        if (!exact_waits) wait_vm<0>();
+        else if (k < D - 1) wait_first<RM, D>(k);
+        else wait_steps<P, D - 2>(nk - 1 - k < D - 2 ? nk - 1 - k : D - 2);
+        gemm::barrier();
+        Half x, y;
+        read(x, S, 0);
+        read(y, S, 1);
+        if (k + D - 1 < nk) {
+            issue_w((S + D - 1) % D, k + D - 1);
+            issue_a((S + D - 1) % D, k + D - 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(x);
+        multiply(y);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    for (int k = 0; k < nk;) run_ring<D>(step, k, nk);
+}
+
+template <int OUT, bool SWIGLU>
+__global__ __launch_bounds__(64 * kWaves)
+void experts_stream_kernel(const ExpertsGemm g)
+{
+    __shared__ __attribute__((aligned(1024))) int8_t pool[kRing];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, q = lane >> 4;
+    ExpertBlock blk;
+    if (!find_block(g.offsets, g.E, g.S, kLgRows, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
+    const int n_end = SWIGLU ? g.N >> 1 : g.N;
+    constexpr int WC = SWIGLU ? 16 : 32;                     // columns of C a wave
+    const int n0 = ((int)(blockIdx.x % g.n_tiles) * kWaves + wave) * WC;
+
+    // weight row r of the wave's 32
+    const int8_t *wsrc[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int r = 8 * j + (lane >> 3);
+        const int n = SWIGLU ? min(n0 + (r & 15), n_end - 1) + (r >> 4) * n_end : min(n0 + r, n_end - 1);
+        wsrc[j] = reinterpret_cast<const int8_t *>(g.B) + (int64_t)blk.e * g.stride_b + (int64_t)n * g.ldb +
+                  (((lane & 7) ^ swz(r)) << 4);
     }
+    // the rows that the plan names are requested before everything else: loads return in order.  Place of the
+    // lane's direct load j of the activation (places behind the last read the first one), and of its row of
+    // the result's fragment m
+    auto place_a = [&](int j) {
+        const int i = blk.row + 16 * j + 4 * wave + (lane >> 4);
+        return i < blk.end ? i : blk.row;
+    };
+    auto place_c = [&](int m) { return min(blk.row + 16 * m + col, blk.end - 1); };
+    int named_a[4], named_c[4];
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        named_a[m] = named_row(g, place_a(m));
+        named_c[m] = named_row(g, place_c(m));
+    }
+    auto a_src = [&](int j) {
+        const int r = 16 * j + 4 * wave + (lane >> 4);
+        return g.A + (int64_t)max(row_from(g, place_a(j), named_a[j]), 0) * g.lda + (((lane & 15) ^ swz(r)) << 4);
+    };
+    v4i acc[2][4];
 #pragma unroll
     for (int f = 0; f < 2; f++)
 #pragma unroll
-        for (int m = 0; m < MT; m++) sums[wave][2 * m + f][lane] = acc[f][m];
-    __syncthreads();
-
-    // lane l of a fragment holds row l % 16 and columns 4 (l / 16) .. +3
-    const bool vec = g.vec;
-    auto total = [&](int p) {
-        v4i t = sums[0][p][lane];
+        for (int m = 0; m < 4; m++) acc[f][m] = v4i{0, 0, 0, 0};
+    // what the epilogue needs is requested behind the first steps: lane l of a fragment holds row l % 16 and
+    // columns 4 (l / 16) .. +3
+    v4f sb[2], bias[2];
+    int to[4];
+    float sa[4];
+    auto request = [&]() {
 #pragma unroll
-        for (int w = 1; w < kWaves; w++) t += sums[w][p][lane];
-        return t >> 4;
+        for (int f = 0; f < 2; f++) {
+            const int n = n0 + (SWIGLU ? 0 : 16 * f) + 4 * q;
+            const int64_t at = (int64_t)blk.e * g.N + n + (SWIGLU ? f * n_end : 0);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                sb[f][r] = OUT != 3 && n + r < n_end ? g.sb[at + r] : 0.0f;
+                bias[f][r] = g.bias && n + r < n_end ? g.bias[at + r] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; m++) {
+            const int i = place_c(m), from = row_from(g, i, named_c[m]);
+            const bool there = blk.row + 16 * m + col < blk.end && from >= 0;
+            to[m] = there ? row_to(g, i, named_c[m]) : -1;
+            sa[m] = OUT != 3 && there ? g.sa[from] : 0.0f;
+        }
     };
-    auto scaled = [&](const v4i &t, float sa, int n, int left) {
+    const int rows = blk.end - blk.row, nk = g.K_pad / 256;
+    if (rows <= 16) stream_products<1, 4>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
+    else if (rows <= 32) stream_products<2, 3>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
+    else stream_products<4, 2>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
+
+    auto scaled = [&](const v4i &t, float s, int f) {
         v4f v;
-        const int64_t at = (int64_t)blk.e * g.N + n;
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-            v[r] = r < left ? ((float)t[r] * sa) * g.sb[at + r] : 0.0f;
-            if (g.bias && r < left) v[r] += g.bias[at + r];
+            v[r] = ((float)t[r] * s) * sb[f][r];
+            if (g.bias) v[r] += bias[f][r];
         }
         return v;
     };
-    for (int p = wave; p < (SWIGLU ? MT : 2 * MT); p += kWaves) {
-        const int m = SWIGLU ? p : p >> 1;
-        const int i = blk.row + 16 * m + col;
-        const int from = i < blk.end ? row_from(g, i) : -1, to = i < blk.end ? row_to(g, i) : -1;
-        const int n = n0 + (SWIGLU ? 0 : 16 * (p & 1)) + 4 * q;
-        const int left = n_end - n;
-        if (from < 0 || to < 0 || left <= 0) continue;
-        const float sa = OUT == 3 ? 0.0f : g.sa[from];
-        const int64_t at = (int64_t)to * g.ldc + n;
+#pragma unroll
+    for (int m = 0; m < 4; m++) {
+        if (to[m] < 0) continue;
+        const int64_t row = (int64_t)to[m] * g.ldc;
         if constexpr (SWIGLU) {
-            const v4f a = scaled(total(2 * m), sa, n, left), b = scaled(total(2 * m + 1), sa, half + n, left);
+            const int n = n0 + 4 * q;
+            if (n >= n_end) continue;
+            const v4f a = scaled(acc[0][m] >> 4, sa[m], 0), b = scaled(acc[1][m] >> 4, sa[m], 1);
             v4f o;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
@@ -160,49 +296,50 @@ void experts_few_kernel(const ExpertsGemm g)
                 // library: without this the compiler makes one rounding of the two (v_fma_mixlo_f16)
                 if constexpr (OUT == 1) asm("" : "+v"(o[r]));
             }
-            store4<OUT>(g.C, at, o, v4i{}, left, vec);
+            store4<OUT>(g.C, row + n, o, v4i{}, n_end - n, g.vec);
         } else {
-            const v4i t = total(p);
-            store4<OUT>(g.C, at, OUT == 3 ? v4f{} : scaled(t, sa, n, left), t, left, vec);
+#pragma unroll
+            for (int f = 0; f < 2; f++) {
+                const int n = n0 + 16 * f + 4 * q;
+                const v4i t = acc[f][m] >> 4;
+                if (n < n_end) store4<OUT>(g.C, row + n, OUT == 3 ? v4f{} : scaled(t, sa[m], f), t, n_end - n, g.vec);
+            }
         }
     }
 }
 
 template <int OUT, bool SWIGLU>
-hipError_t launch_few(const ExpertsGemm &g, int mt, int64_t blocks, hipStream_t st)
+hipError_t launch_stream(const ExpertsGemm &g, hipStream_t st)
 {
-    const dim3 grid((unsigned)(blocks * g.n_tiles)), threads(64 * kWaves);
-    if (mt == 1) hipLaunchKernelGGL((experts_few_kernel<OUT, 1, SWIGLU>), grid, threads, 0, st, g);
-    else hipLaunchKernelGGL((experts_few_kernel<OUT, 2, SWIGLU>), grid, threads, 0, st, g);
+    const dim3 grid((unsigned)(most_blocks(g.S, g.E, kLgRows) * g.n_tiles));
+    hipLaunchKernelGGL((experts_stream_kernel<OUT, SWIGLU>), grid, dim3(64 * kWaves), 0, st, g);
     return hipGetLastError();
 }
 
+// Many rows an expert on average: 256-row tiles, whose waves share the weights in LDS.  64 experts, bf16, us
+// for 3584 x 5376 and 5376 x 1792, by streams and by tiles: 100 rows an expert 240 and 154, 280 and 161;
+// 200 rows 416 and 277, 368 and 207.
+bool tiled(int64_t S, int64_t E) { return S > 112 * E; }
+
 }  // namespace
 
-// Many rows an expert on average: tiles through LDS.
-static bool tiled(int64_t S, int64_t E) { return S > 32 * E; }
-static int lg_rows(int64_t S, int64_t E) { return S <= 16 * E ? 4 : 5; }
-
-int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N, bool)
+int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N)
 {
     if (tiled(S, E)) return 2 * experts_tile_blocks(S, E, N);
-    return most_blocks(S, E, lg_rows(S, E)) * ((N + kTileN - 1) / kTileN);
+    return most_blocks(S, E, kLgRows) * ((N + kTileN - 1) / kTileN);
 }
 
 hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st)
 {
     if (tiled(g.S, g.E)) return launch_experts_tile(g, out_dtype, swiglu, st);
-    const int lg = lg_rows(g.S, g.E);
     g.n_tiles = (g.N + kTileN - 1) / kTileN;
     const int es = out_dtype < 2 ? 2 : 4;
     g.vec = (uintptr_t)g.C % (4 * es) == 0 && g.ldc % 4 == 0;
-    const int64_t blocks = most_blocks(g.S, g.E, lg);
-    const int mt = 1 << (lg - 4);
     switch (out_dtype) {
-    case 0: return swiglu ? launch_few<0, true>(g, mt, blocks, st) : launch_few<0, false>(g, mt, blocks, st);
-    case 1: return swiglu ? launch_few<1, true>(g, mt, blocks, st) : launch_few<1, false>(g, mt, blocks, st);
-    case 2: return swiglu ? launch_few<2, true>(g, mt, blocks, st) : launch_few<2, false>(g, mt, blocks, st);
-    case 3: return swiglu ? hipErrorInvalidValue : launch_few<3, false>(g, mt, blocks, st);
+    case 0: return swiglu ? launch_stream<0, true>(g, st) : launch_stream<0, false>(g, st);
+    case 1: return swiglu ? launch_stream<1, true>(g, st) : launch_stream<1, false>(g, st);
+    case 2: return swiglu ? launch_stream<2, true>(g, st) : launch_stream<2, false>(g, st);
+    case 3: return swiglu ? hipErrorInvalidValue : launch_stream<3, false>(g, st);
     default: return hipErrorInvalidValue;
     }
 }

@@ -95,7 +95,7 @@ void experts_tile_kernel(const ExpertsGemm g)
         const int p = wave * PPW + j;
         if (p < PIECES_A) {
             const int r = 8 * p + (lane >> 3);
-            const int from = row_from(g, blk.row + (r < rows ? r : 0));
+            const int i = blk.row + (r < rows ? r : 0), from = row_from(g, i, named_row(g, i));
             gsrc[j] = g.A + (int64_t)max(from, 0) * g.lda + (((lane & 7) ^ swz_a(r)) << 4);
             ldst[j] = p * 1024;
             kstep[j] = BK;
@@ -112,9 +112,9 @@ void experts_tile_kernel(const ExpertsGemm g)
     float *const map_sa = reinterpret_cast<float *>(pool + MAPS) + BM;
     float *const map_sb = map_sa + BM, *const map_bias = map_sb + BN;
     if (tid < BM) {
-        const int i = blk.row + tid;
-        const int from = tid < rows ? row_from(g, i) : -1, to = tid < rows ? row_to(g, i) : -1;
-        map_to[tid] = from < 0 ? -1 : to;
+        const int i = blk.row + (tid < rows ? tid : 0), named = named_row(g, i);
+        const int from = tid < rows ? row_from(g, i, named) : -1;
+        map_to[tid] = from < 0 ? -1 : row_to(g, i, named);
         map_sa[tid] = OUT != 3 && from >= 0 ? g.sa[from] : 0.0f;
     } else {
         const int r = tid - BM;

@@ -201,7 +201,7 @@ struct ExpertsGemm {
 int64_t experts_tile_blocks(int64_t S, int64_t E, int64_t N);
 hipError_t launch_experts_tile(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);
 // workgroups of the launch, in units of 256 threads
-int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N, bool swiglu);
+int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N);
 hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);
 
 struct CombineLaunch {

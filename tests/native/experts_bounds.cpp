@@ -41,7 +41,7 @@ int main()
                 const int first = block_place(lo, b, lg);
                 require(first >= lo && first < hi, "block");
                 for (int i = first; i < first + (1 << lg) && i < hi; i++) {
-                    const int from = row_from(g, i), to = row_to(g, i);
+                    const int named = named_row(g, i), from = row_from(g, i, named), to = row_to(g, i, named);
                     require(from >= -1 && from < g.M, "row of A");
                     require(to >= -1 && to < S, "row of C");
                     walked++;
