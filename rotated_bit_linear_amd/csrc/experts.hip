@@ -34,20 +34,122 @@ __device__ __forceinline__ uint64_t ordered(double v)
     return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int m) { return __shfl_xor(v, m); }
-
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
+}
+// the value of the other half of 2^(lg + 1) lanes, where each half of 2^lg holds one value: by quads, half
+// rows and rows of 16 lanes, above by a shuffle
+__device__ __forceinline__ double other_half(double v, int lg)
+{
+    switch (lg) {
+    case 0: return dpp<0xB1>(v);                      // quad_perm 1 0 3 2
+    case 1: return dpp<0x4E>(v);                      // quad_perm 2 3 0 1
+    case 2: return dpp<0x141>(v);                     // row_half_mirror
+    case 3: return dpp<0x140>(v);                     // row_mirror
+    default: return __shfl_xor(v, 1 << lg);
+    }
+}
 __device__ __forceinline__ double wave_sum(double v)
 {
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += shfl_xor_f64(v, m);
+    for (int lg = 0; lg < 6; lg++) v += other_half(v, lg);
     return v;
 }
+__device__ __forceinline__ double read_lane(double v, int lane)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
+    return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
+}
+// 1 / d for d >= 1, infinite d included: the instruction's estimate and two Newton steps, within 2^-51
+__device__ __forceinline__ double recip_f64(double d)
+{
+    double y = __builtin_amdgcn_rcp(d);
+    y = fma(fma(-d, y, 1.0), y, y);
+    y = fma(fma(-d, y, 1.0), y, y);
+    return d < 0x1p1000 ? y : 0.0;
+}
 
-// One wave a token; lane l holds experts l, l + 64, ...  Scores are computed in FP64, so that which of
-// two experts is chosen does not turn on a rounding; without a bias the logits order the experts as
-// the scores do, and only the chosen ones' scores are computed.  k times the wave's largest key, the
-// lowest expert where several have it, is taken and struck out.
+// One wave a token; lane l holds experts l, l + 64, ...
+// Which experts are chosen has to follow from the scores in FP64: it must not turn on a rounding.  Without a
+// bias the logits order the experts as the scores do, and are compared themselves.  Otherwise keys (and
+// groups' values) are computed in FP32 first, off by less than kSure / 4 of max(1, |key|); where every two
+// keys whose order matters are further apart than kSure, that order is FP64's, and FP64 computes the chosen
+// experts' scores alone, a lane each.  Where they are not, the token is done again in FP64.  (kSure 2^-17;
+// sigmoid: an exponent's argument off by 2^-24 of it, exponential, addition and reciprocal by 2^-23 each;
+// softmax: a sum of up to 512 powers in 14 levels, 2^-20; the bias' addition 2^-24.)
+// The choice: each lane sorts its own keys, then k times the wave's largest head, the lowest expert where
+// several have it, is taken.  Bound by its instructions: 19989 tokens, 256 experts in 8 groups, sigmoid with a
+// bias, 8 choices 27 us (42 wholly in FP64); 64 experts, softmax 12.
 constexpr int kRouteWaves = 4;
+constexpr float kSure = 0x1p-17f;
+
+__device__ __forceinline__ uint32_t ordered32(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);                     // -0 equals 0
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered32(uint32_t o)
+{
+    return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float other_half(float v, int lg)
+{
+    const int x = (int)__float_as_uint(v);
+    switch (lg) {
+    case 0: return __uint_as_float(__builtin_amdgcn_update_dpp(0, x, 0xB1, 0xF, 0xF, true));
+    case 1: return __uint_as_float(__builtin_amdgcn_update_dpp(0, x, 0x4E, 0xF, 0xF, true));
+    case 2: return __uint_as_float(__builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, true));
+    case 3: return __uint_as_float(__builtin_amdgcn_update_dpp(0, x, 0x140, 0xF, 0xF, true));
+    default: return __shfl_xor(v, 1 << lg);
+    }
+}
+
+// Groups whose experts may be chosen, bit g << lanes_lg for group g, from the experts' values in LDS (-inf
+// where there is none).  sure is cleared where `margin` leaves it open.
+template <bool FUZZY, class F>
+__device__ __forceinline__ uint64_t best_groups(const RouteLaunch &a, const F *values, F margin, int lane, bool &sure)
+{
+    const int size = a.group_size, per = 1 << a.lanes_lg, g = lane >> a.lanes_lg;
+    F b1 = -INFINITY, b2 = -INFINITY;
+    auto second = [](F x, F y) { return x < y ? x : y; };
+    auto first = [](F x, F y) { return x > y ? x : y; };
+    if (g < a.G)
+        for (int x = lane & (per - 1); x < size; x += per) {
+            const F v = values[g * size + x];
+            b2 = first(b2, second(b1, v));
+            b1 = first(b1, v);
+        }
+    for (int lg = 0; lg < a.lanes_lg; lg++) {
+        const F o1 = other_half(b1, lg), o2 = other_half(b2, lg);
+        b2 = first(first(b2, o2), second(b1, o1));
+        b1 = first(b1, o1);
+    }
+    const F v = a.group_sum == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    const F slack = margin * first(F(1), v < 0 ? -v : v);
+    int better = 0, perhaps = 0;                      // groups that come before this one, that may
+    for (int o = 0; o < a.G; o++) {
+        const F w = read_lane(v, o << a.lanes_lg);
+        if constexpr (FUZZY) {
+            better += w > v + slack;
+            perhaps += o != g && w > v - slack;
+        } else {
+            better += w > v || (w == v && o < g);
+        }
+    }
+    if constexpr (FUZZY)
+        sure = sure && __builtin_amdgcn_ballot_w64(g < a.G && perhaps >= a.top_groups && better < a.top_groups) == 0;
+    return __builtin_amdgcn_ballot_w64(g < a.G && better < a.top_groups);
+}
 
 template <int DT, int NE>
 __global__ __launch_bounds__(64 * kRouteWaves)
@@ -58,121 +160,199 @@ void route_kernel(const RouteLaunch a)
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
     if (t >= a.T) return;
     const auto *row = static_cast<const typename Elem<DT>::T *>(a.logits) + t * a.ld;
+    auto wave_fence = [] {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    };
 
-    float l[NE];
-    uint64_t key[NE];
-    double score[NE] = {};
-    uint32_t top = 0;
-    bool valid[NE];
+    // e / group_size for e < 512: the factor is off by less than 2^-20 of one
+    auto group_of = [&](int e) { return e < a.E ? (int)((uint32_t)e * a.group_factor >> 20) : 0; };
+
+    float l[NE], b[NE];
+    uint32_t key[NE], top = 0;
 #pragma unroll
     for (int i = 0; i < NE; i++) {
         const int e = 64 * i + lane;
         l[i] = e < a.E ? Elem<DT>::cvt(row[e]) : -INFINITY;
+        b[i] = a.bias && e < a.E ? a.bias[e] : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < NE; i++) {
-        valid[i] = l[i] > -INFINITY;                  // neither -inf nor NaN
-        const uint32_t b = __float_as_uint(l[i]), o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-        if (valid[i] && o > top) top = o;
-    }
-    top = wave_max(top);
-    const float most = __uint_as_float(top ^ (top >> 31 ? 0x80000000u : 0xFFFFFFFFu));
-    // exp(l - most), 1 where they are equal (infinite or not)
-    auto power = [&](float x) { return x == most ? 1.0 : exp((double)x - (double)most); };
-    auto sigmoid = [&](float x) { return 1.0 / (1.0 + exp(-(double)x)); };
-
     const bool grouped = a.top_groups < a.G;
     const bool all_scores = a.bias || (grouped && a.group_sum == 2);
-    double norm = 1.0;                                // softmax: 1 / sum of the powers
-    if (!a.sigmoid && (all_scores || !a.renorm)) {
-        double sum = 0.0;
+    float most = 0.0f;
+    if (!a.sigmoid) {
 #pragma unroll
         for (int i = 0; i < NE; i++) {
-            score[i] = valid[i] ? power(l[i]) : 0.0;
-            sum += score[i];
+            const uint32_t o = l[i] > -INFINITY ? ordered32(l[i]) : 0u;
+            top = top > o ? top : o;
         }
-        norm = 1.0 / wave_sum(sum);
+        most = unordered32(wave_max(top));
+    }
+    // a logit of -inf or NaN, and a key of either, is never chosen
+    auto valid = [&](int i, auto v) { return l[i] > -INFINITY && v > -INFINITY; };
+    // exp(l - most), 1 where they are equal (infinite or not)
+    auto power = [&](float x) { return x == most ? 1.0 : exp((double)x - (double)most); };
+    auto sigmoid = [&](float x) { return recip_f64(1.0 + exp(-(double)x)); };
+
+    bool sure = true;
+    float value[NE];
+    if (all_scores) {
+        constexpr float log2e = 0x1.715476p+0f;
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < NE; i++)
+                value[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-l[i] * log2e));
+        } else {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                value[i] = l[i] == most ? 1.0f : l[i] > -INFINITY ? __builtin_amdgcn_exp2f((l[i] - most) * log2e) : 0.0f;
+                sum += value[i];
+            }
+#pragma unroll
+            for (int lg = 0; lg < 6; lg++) sum += other_half(sum, lg);
+            sum = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+            for (int i = 0; i < NE; i++) value[i] *= sum;
+        }
+#pragma unroll
+        for (int i = 0; i < NE; i++) value[i] += b[i];
     }
 #pragma unroll
     for (int i = 0; i < NE; i++) {
-        const int e = 64 * i + lane;
-        double v = (double)l[i];
-        if (all_scores) {
-            score[i] = !valid[i] ? 0.0 : a.sigmoid ? sigmoid(l[i]) : score[i] * norm;
-            if (a.bias) v = score[i] + (double)(valid[i] ? a.bias[e] : 0.0f);
-        }
-        valid[i] = valid[i] && v > -INFINITY;
-        key[i] = valid[i] ? ordered(v) : 0;
-        if (grouped) {
-            if (a.group_sum == 2 && !a.bias) v = score[i];
-            if (e < a.E) lds[wave * a.E + e] = valid[i] ? v : -INFINITY;
-        }
+        const float v = a.bias ? value[i] : l[i];
+        key[i] = valid(i, v) ? ordered32(v) : 0u;
     }
     if (grouped) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        // 2^lanes_lg lanes a group: its largest and second largest value
-        const int size = a.E / a.G, per = 1 << a.lanes_lg, g = lane >> a.lanes_lg;
-        double b1 = -INFINITY, b2 = -INFINITY;
-        if (g < a.G)
-            for (int x = lane & (per - 1); x < size; x += per) {
-                const double v = lds[wave * a.E + g * size + x];
-                b2 = fmax(b2, fmin(b1, v));
-                b1 = fmax(b1, v);
-            }
-        for (int m = 1; m < per; m <<= 1) {
-            const double o1 = shfl_xor_f64(b1, m), o2 = shfl_xor_f64(b2, m);
-            b2 = fmax(fmax(b2, o2), fmin(b1, o1));
-            b1 = fmax(b1, o1);
-        }
-        const double v = a.group_sum == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-        int better = 0;                               // groups that come before this one
-        for (int o = 0; o < a.G; o++) {
-            const double w = __shfl(v, o << a.lanes_lg);
-            better += w > v || (w == v && o < g);
-        }
-        const uint64_t kept = __builtin_amdgcn_ballot_w64(g < a.G && better < a.top_groups);
+        float *values = reinterpret_cast<float *>(lds + wave * a.E);
 #pragma unroll
         for (int i = 0; i < NE; i++) {
             const int e = 64 * i + lane;
-            if (e < a.E && !(kept >> ((e / size) << a.lanes_lg) & 1)) key[i] = 0;
+            const float v = all_scores ? value[i] : l[i];
+            if (e < a.E) values[e] = valid(i, v) ? v : -INFINITY;
+        }
+        wave_fence();
+        const uint64_t kept = all_scores ? best_groups<true>(a, values, kSure, lane, sure)
+                                         : best_groups<false>(a, values, 0.0f, lane, sure);
+#pragma unroll
+        for (int i = 0; i < NE; i++) {
+            const int e = 64 * i + lane;
+            if (!(kept >> (group_of(e) << a.lanes_lg) & 1)) key[i] = 0;
         }
     }
 
     int id = -1;                                      // lane j: choice j
-    float chosen = 0.0f;
-    double s = 0.0;
-    for (int j = 0; j < a.k; j++) {
-        uint64_t best = key[0];
-        int at = 0;
-        float bl = l[0];
-        double bs = score[0];
+    if (sure) {
+        // each lane's keys from the largest down, with the places that they come from
+        int at[NE];
 #pragma unroll
-        for (int i = 1; i < NE; i++)
-            if (key[i] > best) { best = key[i]; at = i; bl = l[i]; bs = score[i]; }
-        const uint32_t hi = wave_max((uint32_t)(best >> 32));
-        if (hi == 0) break;                           // none left (a number's key has a bit above)
-        bool mine = (uint32_t)(best >> 32) == hi;
-        const uint32_t lo = wave_max(mine ? (uint32_t)best : 0u);
-        mine = mine && (uint32_t)best == lo;
-        const uint32_t inv = wave_max(mine ? ~(uint32_t)(64 * at + lane) : 0u);
-        const int e = (int)~inv, from = e & 63;
+        for (int i = 0; i < NE; i++) at[i] = i;
+        auto exchange = [&](int x, int y) {
+            const bool swap = key[x] < key[y] || (key[x] == key[y] && at[x] > at[y]);
+            const uint32_t k0 = key[x], k1 = key[y];
+            const int a0 = at[x], a1 = at[y];
+            key[x] = swap ? k1 : k0; key[y] = swap ? k0 : k1;
+            at[x] = swap ? a1 : a0; at[y] = swap ? a0 : a1;
+        };
+        if constexpr (NE == 2) exchange(0, 1);
+        if constexpr (NE >= 4) {
 #pragma unroll
-        for (int i = 0; i < NE; i++)
-            if (64 * i + lane == e) key[i] = 0;
-        const float wl = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bl), from));
-        const uint64_t bits = (uint64_t)__double_as_longlong(bs);
-        const uint32_t s0 = __builtin_amdgcn_readlane((uint32_t)bits, from);
-        const uint32_t s1 = __builtin_amdgcn_readlane((uint32_t)(bits >> 32), from);
-        if (lane == j) {
-            id = e;
-            chosen = wl;
-            s = __longlong_as_double((int64_t)((uint64_t)s1 << 32 | s0));
+            for (int o = 0; o < NE; o += 4) {
+                exchange(o, o + 1); exchange(o + 2, o + 3); exchange(o, o + 2); exchange(o + 1, o + 3); exchange(o + 1, o + 2);
+            }
+        }
+        if constexpr (NE == 8) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) exchange(i, i + 4);
+            exchange(2, 4); exchange(3, 5);
+            exchange(1, 2); exchange(3, 4); exchange(5, 6);
+        }
+        float last = INFINITY;
+        for (int j = 0; j <= a.k; j++) {              // one more than is chosen: is the border clear
+            const uint32_t best = wave_max(key[0]);
+            if (best == 0) break;                     // none left
+            if (a.bias) {
+                const float v = unordered32(best);
+                sure = sure && last - v > kSure * fmaxf(1.0f, fabsf(v));
+                last = v;
+            }
+            if (j == a.k) break;
+            uint64_t have = __builtin_amdgcn_ballot_w64(key[0] == best);
+            int from = __builtin_ctzll(have);
+            int e = 64 * __builtin_amdgcn_readlane(at[0], from) + from;
+            if (have & (have - 1)) {                  // several lanes: the lowest expert
+                e = (int)~wave_max(key[0] == best ? ~(uint32_t)(64 * at[0] + lane) : 0u);
+                from = e & 63;
+            }
+            id = lane == j ? e : id;
+            const bool mine = lane == from;
+#pragma unroll
+            for (int i = 0; i + 1 < NE; i++) {
+                key[i] = mine ? key[i + 1] : key[i];
+                at[i] = mine ? at[i + 1] : at[i];
+            }
+            key[NE - 1] = mine ? 0u : key[NE - 1];
+        }
+        sure = __builtin_amdgcn_readfirstlane(sure);
+    }
+    double norm = 1.0;                                // softmax: 1 / sum of the powers
+    if (!a.sigmoid && (!a.renorm || !sure)) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NE; i++) sum += l[i] > -INFINITY ? power(l[i]) : 0.0;
+        norm = 1.0 / wave_sum(sum);
+    }
+    if (!sure) {
+        uint32_t hi[NE], lo[NE];
+        double exact[NE];
+#pragma unroll
+        for (int i = 0; i < NE; i++) {
+            exact[i] = (a.sigmoid ? sigmoid(l[i]) : power(l[i]) * norm) + (double)b[i];
+            const double v = a.bias ? exact[i] : (double)l[i];
+            const uint64_t k = ordered(v);
+            hi[i] = valid(i, v) ? (uint32_t)(k >> 32) : 0u;           // a number's upper half is not 0
+            lo[i] = (uint32_t)k;
+        }
+        if (grouped) {
+            double *values = lds + wave * a.E;
+            wave_fence();
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                const int e = 64 * i + lane;
+                if (e < a.E) values[e] = hi[i] ? exact[i] : -INFINITY;
+            }
+            wave_fence();
+            const uint64_t kept = best_groups<false>(a, values, 0.0, lane, sure);
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                const int e = 64 * i + lane;
+                if (!(kept >> (group_of(e) << a.lanes_lg) & 1)) hi[i] = 0;
+            }
+        }
+        id = -1;
+        for (int j = 0; j < a.k; j++) {
+            uint32_t best = 0, low = 0, inv = 0;
+#pragma unroll
+            for (int i = 0; i < NE; i++) best = best > hi[i] ? best : hi[i];
+            best = wave_max(best);
+            if (best == 0) break;
+#pragma unroll
+            for (int i = 0; i < NE; i++) low = hi[i] == best && lo[i] > low ? lo[i] : low;
+            low = wave_max(low);
+#pragma unroll
+            for (int i = 0; i < NE; i++) {
+                const uint32_t x = ~(uint32_t)(64 * i + lane);
+                inv = hi[i] == best && lo[i] == low && x > inv ? x : inv;
+            }
+            const int e = (int)~wave_max(inv);
+#pragma unroll
+            for (int i = 0; i < NE; i++) hi[i] = 64 * i + lane == e ? 0u : hi[i];
+            id = lane == j ? e : id;
         }
     }
-    if (!all_scores) s = id < 0 ? 0.0 : a.sigmoid ? sigmoid(chosen) : power(chosen) * norm;
-    if (id < 0) s = 0.0;
+    // the chosen experts' own scores, a lane each
+    const float chosen = id < 0 ? 0.0f : Elem<DT>::cvt(row[id]);
+    const double s = id < 0 ? 0.0 : a.sigmoid ? sigmoid(chosen) : power(chosen) * norm;
     double w = s * (double)a.scale;
     if (a.renorm) {
         const double sum = wave_sum(s);
@@ -299,22 +479,23 @@ template <> __device__ __forceinline__ uint32_t round_to<0>(float v) { return __
 template <> __device__ __forceinline__ uint32_t round_to<1>(float v) { return __half_as_ushort(__float2half(v)); }
 template <> __device__ __forceinline__ uint32_t round_to<2>(float v) { return __float_as_uint(v); }
 
-// V elements of a row in one access
-template <int DT, int V>
+// 16 bytes of a row in one access, wherever the row begins: rows are element-aligned, and the hardware takes
+// such an access at any address.  Elements past the row's end are neither read nor written.
+template <int DT>
 struct Piece {
-    static constexpr int ES = DT == 2 ? 4 : 2, B = V * ES;
     typedef typename Elem<DT>::T T;
+    static constexpr int V = 16 / (int)sizeof(T);
     typedef T Vec __attribute__((ext_vector_type(V)));
+    typedef Vec Loose __attribute__((aligned(sizeof(T))));
     T e[V];
-    __device__ __forceinline__ void load(const T *p, int left)
+    __device__ __forceinline__ void load(const T *p, int left, bool past)
     {
         if (left >= V) {
-            if constexpr (V == 1) e[0] = *p;
-            else {
-                const Vec v = *reinterpret_cast<const Vec *>(p);
+            Vec v;
+            if (past) v = __builtin_nontemporal_load(reinterpret_cast<const Loose *>(p));
+            else v = *reinterpret_cast<const Loose *>(p);
 #pragma unroll
-                for (int i = 0; i < V; i++) e[i] = v[i];
-            }
+            for (int i = 0; i < V; i++) e[i] = v[i];
         } else {
 #pragma unroll
             for (int i = 0; i < V; i++) e[i] = i < left ? p[i] : (T)0;
@@ -323,13 +504,10 @@ struct Piece {
     __device__ __forceinline__ void store(T *p, int left) const
     {
         if (left >= V) {
-            if constexpr (V == 1) *p = e[0];
-            else {
-                Vec v;
+            Vec v;
 #pragma unroll
-                for (int i = 0; i < V; i++) v[i] = e[i];
-                *reinterpret_cast<Vec *>(p) = v;
-            }
+            for (int i = 0; i < V; i++) v[i] = e[i];
+            *reinterpret_cast<Loose *>(p) = v;
         } else {
 #pragma unroll
             for (int i = 0; i < V; i++)
@@ -338,46 +516,52 @@ struct Piece {
     }
 };
 
-// Threads take V columns of one token; the rows of up to kAhead choices are requested before the first
-// is used.  Bound by HBM.
-constexpr int kCombineThreads = 256, kAhead = 8;
+// A wave takes 64 pieces of 16 bytes of one token's row; the rows of up to kAhead choices are requested
+// before the first is used.  Rows that the last cache does not hold are read past the caches (3000 tokens, 8 rows
+// of 4096 FP32: 85 -> 74 us), others may still lie there (64 tokens: 4.4 us, not 5.5).  Bound by HBM: 19989
+// tokens, 8 rows of 5376 bf16 with a residual 384 us, 5.6 TB/s.
+constexpr int kCombineWaves = 4, kAhead = 8;
 
-template <int DT, int V>
-__global__ __launch_bounds__(kCombineThreads)
+template <int DT>
+__global__ __launch_bounds__(64 * kCombineWaves)
 void combine_kernel(const CombineLaunch a)
 {
-    typedef typename Elem<DT>::T T;
-    const int64_t t = blockIdx.x / (uint32_t)a.pieces;
-    const int n = ((int)(blockIdx.x % (uint32_t)a.pieces) * kCombineThreads + (int)threadIdx.x) * V;
+    using P = Piece<DT>;
+    typedef typename P::T T;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t task = blockIdx.x * (uint32_t)kCombineWaves + wave;
+    const int64_t t = task / (uint32_t)a.pieces;
+    if (t >= a.T) return;
+    const int n = ((int)(task % (uint32_t)a.pieces) * 64 + lane) * P::V;
     const int left = a.N - n;
     if (left <= 0) return;
-    float sum[V];
+    float sum[P::V];
 #pragma unroll
-    for (int i = 0; i < V; i++) sum[i] = 0.0f;
+    for (int i = 0; i < P::V; i++) sum[i] = 0.0f;
     const int32_t *ids = a.ids + t * a.k;
     const float *weights = a.weights + t * a.k;
     const T *y = static_cast<const T *>(a.y) + t * a.k * a.ld_y + n;
-    Piece<DT, V> res;
-    if (a.residual) res.load(static_cast<const T *>(a.residual) + t * a.ld_res + n, left);
+    P res;
+    if (a.residual) res.load(static_cast<const T *>(a.residual) + t * a.ld_res + n, left, false);
     for (int j0 = 0; j0 < a.k; j0 += kAhead) {
-        Piece<DT, V> p[kAhead];
+        P p[kAhead];
         bool here[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; j++) {
             here[j] = j0 + j < a.k && (uint32_t)ids[j0 + j] - (uint32_t)a.first < (uint32_t)a.E;
-            if (here[j]) p[j].load(y + (j0 + j) * a.ld_y, left);
+            if (here[j]) p[j].load(y + (j0 + j) * a.ld_y, left, a.past);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; j++)
             if (here[j]) {
                 const float w = weights[j0 + j];
 #pragma unroll
-                for (int i = 0; i < V; i++) sum[i] = fmaf(w, Elem<DT>::cvt(p[j].e[i]), sum[i]);
+                for (int i = 0; i < P::V; i++) sum[i] = fmaf(w, Elem<DT>::cvt(p[j].e[i]), sum[i]);
             }
     }
-    Piece<DT, V> o;
+    P o;
 #pragma unroll
-    for (int i = 0; i < V; i++) {
+    for (int i = 0; i < P::V; i++) {
         if (a.residual) sum[i] += Elem<DT>::cvt(res.e[i]);
         const uint32_t b = round_to<DT>(sum[i]);
         if constexpr (DT == 2) o.e[i] = __uint_as_float(b);
@@ -386,34 +570,16 @@ void combine_kernel(const CombineLaunch a)
     o.store(static_cast<T *>(a.out) + t * a.ld_out + n, left);
 }
 
-template <int DT, int V>
+template <int DT>
 hipError_t launch_combine_of(CombineLaunch a, hipStream_t st)
 {
-    a.pieces = (a.N + kCombineThreads * V - 1) / (kCombineThreads * V);
-    hipLaunchKernelGGL((combine_kernel<DT, V>), dim3((unsigned)(a.T * a.pieces)), dim3(kCombineThreads), 0, st, a);
+    constexpr int cols = 64 * Piece<DT>::V;
+    a.pieces = (a.N + cols - 1) / cols;
+    a.past = a.T * a.k > (int64_t)(256 << 20) / (int64_t)sizeof(typename Elem<DT>::T) / a.N;
+    const int64_t waves = a.T * a.pieces;
+    hipLaunchKernelGGL((combine_kernel<DT>), dim3((unsigned)((waves + kCombineWaves - 1) / kCombineWaves)),
+                       dim3(64 * kCombineWaves), 0, st, a);
     return hipGetLastError();
-}
-
-// elements that every row's start allows in one access of at most 16 bytes
-int combine_elements(const CombineLaunch &a, int es)
-{
-    uintptr_t bits = (uintptr_t)a.y | (uintptr_t)a.out | (uintptr_t)(a.ld_y * es) | (uintptr_t)(a.ld_out * es);
-    if (a.residual) bits |= (uintptr_t)a.residual | (uintptr_t)(a.ld_res * es);
-    const int bytes = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-    return bytes / es;
-}
-
-template <int DT>
-hipError_t launch_combine_dt(const CombineLaunch &a, hipStream_t st)
-{
-    switch (combine_elements(a, DT == 2 ? 4 : 2)) {
-    case 1: return launch_combine_of<DT, 1>(a, st);
-    case 2: return launch_combine_of<DT, 2>(a, st);
-    case 4: return launch_combine_of<DT, 4>(a, st);
-    default:
-        if constexpr (DT == 2) return hipErrorInvalidValue;
-        else return launch_combine_of<DT, 8>(a, st);
-    }
 }
 
 }  // namespace
@@ -422,6 +588,8 @@ hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st)
 {
     a.lanes_lg = 0;
     while ((2 << a.lanes_lg) * a.G <= 64) a.lanes_lg++;
+    a.group_size = a.E / a.G;
+    a.group_factor = ((1u << 20) + a.group_size - 1) / a.group_size;
     switch (dtype) {
     case 0: return launch_route_of<0>(a, st);
     case 1: return launch_route_of<1>(a, st);
@@ -430,13 +598,14 @@ hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st)
     }
 }
 
-// Runs of 2048 slots above 8192, so that a clip's 160 thousand fill a third of the device; at most 256
-// runs, whose counts every workgroup adds up.
+// One workgroup for 4096 slots, above runs of 1024 (8192 slots: 5.7 us, 8.7 by one workgroup) and, where the
+// counts of the runs before become the longer part, of 4096 (160 thousand slots: 9.9 us, 12.8 with 1024);
+// at most 256 runs.
 void plan_runs(int64_t S, int64_t &runs, int64_t &run)
 {
     constexpr int64_t step = 64 * kPlanWaves;
     if (S < 1) S = 1;
-    runs = S <= 8192 ? 1 : (S + 2047) / 2048;
+    runs = S <= 4096 ? 1 : S <= 65536 ? (S + 1023) / 1024 : (S + 4095) / 4096;
     if (runs > 256) runs = 256;
     run = ((S + runs - 1) / runs + step - 1) / step * step;
     runs = (S + run - 1) / run;
@@ -460,9 +629,9 @@ hipError_t launch_experts_plan(PlanLaunch a, hipStream_t st)
 hipError_t launch_experts_combine(const CombineLaunch &a, int dtype, hipStream_t st)
 {
     switch (dtype) {
-    case 0: return launch_combine_dt<0>(a, st);
-    case 1: return launch_combine_dt<1>(a, st);
-    case 2: return launch_combine_dt<2>(a, st);
+    case 0: return launch_combine_of<0>(a, st);
+    case 1: return launch_combine_of<1>(a, st);
+    case 2: return launch_combine_of<2>(a, st);
     default: return hipErrorInvalidValue;
     }
 }

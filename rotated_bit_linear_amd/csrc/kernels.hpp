@@ -165,7 +165,9 @@ struct RouteLaunch {
     int sigmoid, renorm;
     int32_t *ids;
     float *weights;
-    int lanes_lg;            // set by the launcher: log2 of the lanes that share a group
+    int lanes_lg;            // set by the launcher: log2 of the lanes that share a group,
+    int group_size;          // experts a group,
+    uint32_t group_factor;   // 2^20 / group_size, rounded up
 };
 hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st);
 
@@ -214,7 +216,7 @@ struct CombineLaunch {
     int64_t ld_res;
     void *out;
     int64_t ld_out;
-    int pieces;              // set by the launcher: workgroups a token
+    int pieces, past;        // set by the launcher: waves a token, y past the caches
 };
 hipError_t launch_experts_combine(const CombineLaunch &a, int dtype, hipStream_t st);
 
