@@ -59,16 +59,18 @@ __device__ __forceinline__ void store4(void *C, int64_t at, const v4f &v, const 
     }
 }
 
-// A workgroup takes up to 64 rows of an expert and 128 weight rows, 32 a wave (with SwiGLU 16 gates and
-// their 16 values), and walks K in steps of 256 codes: whole lines of the weight.  Loaded to registers in the
-// order of the matrix instruction, neighbouring lanes would take 16 bytes of different rows, which the
-// texture unit works off a lane's line at a time; so both operands go to LDS by direct loads in which eight
-// (weight) and sixteen (activation) lanes share a row.  A wave's weight rows are its own, the activation's
-// are shared: one barrier a step.  The ring's 80 KB let two workgroups run on a compute unit; how many
-// steps fit follows from the rows that there are: 4 steps for up to 16 rows, 3 for 32, 2 for 64.
+// A workgroup takes up to 64 rows of an expert and 128 weight rows, 32 a wave (with SwiGLU 16 gates and their
+// 16 values), and walks K in steps of 256 codes: whole lines of the weight.  Loaded to registers in the order
+// of the matrix instruction, neighbouring lanes would take 16 bytes of different rows, which the texture unit
+// works off a lane's line at a time; so both operands go to LDS by direct loads in which eight (weight) and
+// sixteen (activation) lanes share a row.  A wave's weight rows are its own, the activation's are shared: one
+// barrier a step.  The ring's 72 KB let two workgroups run on a compute unit: 3 steps for up to 32 rows, 2 for
+// 64.  (One workgroup with twice the ring, or several tiles of weight rows a workgroup without a pause between
+// them: slower; 64 tokens on 64 experts, 5376 x 1792: 57 us, 110 and 59.)
 constexpr int kWaves = 4, kTileN = 32 * kWaves, kLgRows = 6;
 constexpr int kStepW = kTileN * 128;                  // LDS bytes of a step's weight rows
-constexpr int kRing = 80 * 1024;
+constexpr int kRing = 72 * 1024;
+constexpr int kScales = 512;                          // LDS bytes a wave: scales and biases of its weight rows
 
 __device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3 & 1)) & 7; }
 
@@ -94,53 +96,103 @@ __device__ __forceinline__ void wait_first(int k)
     else wait_first<RM, D, J + 1>(k);
 }
 
-// steps k .. of a ring, one stage after another
-template <int D, int S = 0, class Step>
-__device__ __forceinline__ void run_ring(Step &step, int &k, int nk)
-{
-    if constexpr (S < D) {
-        if (k >= nk) return;
-        step(std::integral_constant<int, S>{}, k++);
-        run_ring<D, S + 1>(step, k, nk);
-    }
-}
+// What a workgroup of the stream kernel does, the same for every number of rows.
+struct Stream {
+    const ExpertsGemm &g;
+    ExpertBlock blk;
+    int tile;                // which 128 weight rows
+    int lane, wave;
+    int8_t *pool;
+};
 
-// The products of 16 RM rows over a ring of D steps.  wsrc: the lane's source of each of the wave's four
-// direct loads of a step; a_src(j): of its load j of the activation.  once: nobody else reads these weight
-// rows, so they go past the caches (64 tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an
-// expert has several blocks its weights come from the cache the next time (777 tokens on 60: 31 us, not 36).
-template <int RM, int D, class Source, class Request>
-__device__ __forceinline__ void stream_products(int8_t *pool, const int8_t *(&wsrc)[4], Source a_src, Request request,
-                                                bool once, int nk, int wave, int lane, v4i (&acc)[2][4])
+// Products of up to 16 RM rows over a ring of D steps.  Weights that nobody else reads go past the caches (64
+// tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an expert has several blocks its weights
+// come from the cache the next time (777 tokens on 60: 31 us, not 36).
+template <int OUT, bool SWIGLU, int RM, int D>
+__device__ __forceinline__ void stream(const Stream &x)
 {
     constexpr int STEP = kStepW + RM * 4096, P = 4 + RM;     // LDS bytes, and direct loads a wave, of a step
     static_assert(D * STEP <= kRing && D >= 2, "ring");
-    const int col = lane & 15, q = lane >> 4;
-    auto issue_w = [&](int s, int k) {
+    constexpr int WC = SWIGLU ? 16 : 32;                     // columns of C a wave
+    const ExpertsGemm &g = x.g;
+    const ExpertBlock blk = x.blk;
+    const int lane = x.lane, wave = x.wave, col = lane & 15, q = lane >> 4;
+    int8_t *const pool = x.pool, *const scales = pool + kRing + wave * kScales;
+    const int n_end = SWIGLU ? g.N >> 1 : g.N, nk = g.K_pad / 256;
+    const int n0 = (x.tile * kWaves + wave) * WC;
+    const bool once = blk.blocks == 1;
+
+    // the rows that the plan names are requested before everything else: loads return in order.  Place of the
+    // lane's direct load j of the activation (places behind the last read the first one), and of its row of
+    // the result's fragment m
+    auto place_a = [&](int j) {
+        const int i = blk.row + 16 * j + 4 * wave + (lane >> 4);
+        return i < blk.end ? i : blk.row;
+    };
+    auto place_c = [&](int m) { return min(blk.row + 16 * m + col, blk.end - 1); };
+    int named_a[4], named_c[4];
+#pragma unroll
+    for (int m = 0; m < RM; m++) {
+        named_a[m] = named_row(g, place_a(m));
+        named_c[m] = named_row(g, place_c(m));
+    }
+
+    auto weight_row = [&](int r) {                           // row r of the wave's 32
+        return SWIGLU ? min(n0 + (r & 15), n_end - 1) + (r >> 4) * n_end : min(n0 + r, n_end - 1);
+    };
+    const int8_t *wsrc[4];                                   // where the next step lies
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int r = 8 * j + (lane >> 3);
+        wsrc[j] = reinterpret_cast<const int8_t *>(g.B) + (int64_t)blk.e * g.stride_b + (int64_t)weight_row(r) * g.ldb +
+                  (((lane & 7) ^ swz(r)) << 4);
+    }
+    auto issue_w = [&](int at) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const int8_t *src = wsrc[j] + (int64_t)k * 128;
-            int8_t *dst = pool + s * STEP + wave * 4096 + j * 1024;
-            if (once) __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 2);     // non-temporal
-            else __builtin_amdgcn_global_load_lds(src, dst, 16, 0, 0);
+            int8_t *dst = pool + at + wave * 4096 + j * 1024;
+            if (once) __builtin_amdgcn_global_load_lds(wsrc[j], dst, 16, 0, 2);     // non-temporal
+            else __builtin_amdgcn_global_load_lds(wsrc[j], dst, 16, 0, 0);
+            wsrc[j] += 128;
         }
     };
 #pragma unroll
     for (int s = 0; s < D - 1; s++)
-        if (s < nk) issue_w(s, s);
+        if (s < nk) issue_w(s * STEP);
+
     const int8_t *asrc[4];
 #pragma unroll
-    for (int j = 0; j < RM; j++) asrc[j] = a_src(j);
-    auto issue_a = [&](int s, int k) {
+    for (int j = 0; j < RM; j++) {
+        const int r = 16 * j + 4 * wave + (lane >> 4);
+        asrc[j] = g.A + (int64_t)max(row_from(g, place_a(j), named_a[j]), 0) * g.lda + (((lane & 15) ^ swz(r)) << 4);
+    }
+    auto issue_a = [&](int at) {
 #pragma unroll
-        for (int j = 0; j < RM; j++)
-            __builtin_amdgcn_global_load_lds(asrc[j] + (int64_t)k * 256,
-                                             pool + s * STEP + kStepW + j * 4096 + wave * 1024, 16, 0, 0);
+        for (int j = 0; j < RM; j++) {
+            __builtin_amdgcn_global_load_lds(asrc[j], pool + at + kStepW + j * 4096 + wave * 1024, 16, 0, 0);
+            asrc[j] += 256;
+        }
     };
 #pragma unroll
     for (int s = 0; s < D - 1; s++)
-        if (s < nk) issue_a(s, s);
-    request();
+        if (s < nk) issue_a(s * STEP);
+
+    // what the epilogue needs: scales (and biases) of the weight rows, a lane each, to this wave's LDS; of the
+    // rows to registers
+    if constexpr (OUT != 3) {
+        const int64_t at = (int64_t)blk.e * g.N + weight_row(lane & 31);
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const int8_t *>(g.sb + at), scales, 4, 0, 0);
+        if (g.bias) __builtin_amdgcn_global_load_lds(reinterpret_cast<const int8_t *>(g.bias + at), scales + 256, 4, 0, 0);
+    }
+    int to[4];
+    float sa[4];
+#pragma unroll
+    for (int m = 0; m < RM; m++) {
+        const int i = place_c(m), from = row_from(g, i, named_c[m]);
+        const bool there = blk.row + 16 * m + col < blk.end && from >= 0;
+        to[m] = there ? row_to(g, i, named_c[m]) : -1;
+        sa[m] = OUT != 3 && there ? g.sa[from] : 0.0f;
+    }
 
     // LDS addresses of stage 0: weight chunk 4 t + q of row 16 f + col; activation chunk 8 t + 4 (q / 2) +
     // q % 2 + 2 h of row 16 m + col (h: which of a chunk's two groups of codes)
@@ -154,123 +206,67 @@ __device__ __forceinline__ void stream_products(int8_t *pool, const int8_t *(&ws
             adr_a[t][h] = base + kStepW + col * 256 + (((8 * t + 4 * (q >> 1) + (q & 1) + 2 * h) ^ swz(col)) << 4);
     }
     auto lds = [](uint32_t a) { return *reinterpret_cast<const __attribute__((address_space(3))) v4i *>(a); };
-    struct Half { v4i w[2], a[4][2]; };
-    auto read = [&](Half &x, int s, int t) {
+    v4i acc[2][RM];
 #pragma unroll
-        for (int f = 0; f < 2; f++) x.w[f] = lds(adr_w[t] + s * STEP + f * 2048);
+    for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int m = 0; m < RM; m++) acc[f][m] = v4i{0, 0, 0, 0};
+    struct Half { v4i w[2], a[RM][2]; };
+    auto read = [&](Half &h_, uint32_t at, int t) {
+#pragma unroll
+        for (int f = 0; f < 2; f++) h_.w[f] = lds(adr_w[t] + at + f * 2048);
 #pragma unroll
         for (int m = 0; m < RM; m++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) x.a[m][h] = lds(adr_a[t][h] + s * STEP + m * 4096);
+            for (int h = 0; h < 2; h++) h_.a[m][h] = lds(adr_a[t][h] + at + m * 4096);
     };
-    auto multiply = [&](const Half &x) {
+    auto multiply = [&](const Half &h_) {
 #pragma unroll
         for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int f = 0; f < 2; f++) {
-                const v4i wide = widen((uint32_t)x.w[f][2 * h], (uint32_t)x.w[f][2 * h + 1]);
+                const v4i wide = widen((uint32_t)h_.w[f][2 * h], (uint32_t)h_.w[f][2 * h + 1]);
 #pragma unroll
                 for (int m = 0; m < RM; m++)
-                    acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wide, x.a[m][h], acc[f][m], 0, 0, 0);
+                    acc[f][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wide, h_.a[m][h], acc[f][m], 0, 0, 0);
             }
     };
+
+    // From 2 (D - 1) steps on, waits leave the steps behind the next one in flight; the loads for the epilogue
+    // in between only make the first ones wait for more.
     const bool exact_waits = nk >= 2 * (D - 1);
-    auto step = [&](auto S_, int k) {
-        constexpr int S = decltype(S_)::value;
+    int at = 0, ahead = (D - 1) * STEP;
+    for (int k = 0; k < nk; k++) {
         // step k's loads are done: this wave's, and behind the barrier all; and all have read step k - 1
         if (!exact_waits) wait_vm<0>();
         else if (k < D - 1) wait_first<RM, D>(k);
-        else wait_steps<P, D - 2>(nk - 1 - k < D - 2 ? nk - 1 - k : D - 2);
+        else wait_steps<P, D - 2>(min(nk - 1 - k, D - 2));
         gemm::barrier();
-        Half x, y;
-        read(x, S, 0);
-        read(y, S, 1);
+        asm volatile("" ::: "memory");                       // no read of LDS before the barrier
+        Half a, b;
+        read(a, at, 0);
+        read(b, at, 1);
         if (k + D - 1 < nk) {
-            issue_w((S + D - 1) % D, k + D - 1);
-            issue_a((S + D - 1) % D, k + D - 1);
+            issue_w(ahead);
+            issue_a(ahead);
         }
         __builtin_amdgcn_sched_barrier(0);
-        multiply(x);
-        multiply(y);
+        multiply(a);
+        multiply(b);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    };
-    for (int k = 0; k < nk;) run_ring<D>(step, k, nk);
-}
-
-template <int OUT, bool SWIGLU>
-__global__ __launch_bounds__(64 * kWaves)
-void experts_stream_kernel(const ExpertsGemm g)
-{
-    __shared__ __attribute__((aligned(1024))) int8_t pool[kRing];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, q = lane >> 4;
-    ExpertBlock blk;
-    if (!find_block(g.offsets, g.E, g.S, kLgRows, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
-    const int n_end = SWIGLU ? g.N >> 1 : g.N;
-    constexpr int WC = SWIGLU ? 16 : 32;                     // columns of C a wave
-    const int n0 = ((int)(blockIdx.x % g.n_tiles) * kWaves + wave) * WC;
-
-    // weight row r of the wave's 32
-    const int8_t *wsrc[4];
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const int r = 8 * j + (lane >> 3);
-        const int n = SWIGLU ? min(n0 + (r & 15), n_end - 1) + (r >> 4) * n_end : min(n0 + r, n_end - 1);
-        wsrc[j] = reinterpret_cast<const int8_t *>(g.B) + (int64_t)blk.e * g.stride_b + (int64_t)n * g.ldb +
-                  (((lane & 7) ^ swz(r)) << 4);
+        at = at == (D - 1) * STEP ? 0 : at + STEP;
+        ahead = ahead == (D - 1) * STEP ? 0 : ahead + STEP;
     }
-    // the rows that the plan names are requested before everything else: loads return in order.  Place of the
-    // lane's direct load j of the activation (places behind the last read the first one), and of its row of
-    // the result's fragment m
-    auto place_a = [&](int j) {
-        const int i = blk.row + 16 * j + 4 * wave + (lane >> 4);
-        return i < blk.end ? i : blk.row;
-    };
-    auto place_c = [&](int m) { return min(blk.row + 16 * m + col, blk.end - 1); };
-    int named_a[4], named_c[4];
-#pragma unroll
-    for (int m = 0; m < 4; m++) {
-        named_a[m] = named_row(g, place_a(m));
-        named_c[m] = named_row(g, place_c(m));
-    }
-    auto a_src = [&](int j) {
-        const int r = 16 * j + 4 * wave + (lane >> 4);
-        return g.A + (int64_t)max(row_from(g, place_a(j), named_a[j]), 0) * g.lda + (((lane & 15) ^ swz(r)) << 4);
-    };
-    v4i acc[2][4];
-#pragma unroll
-    for (int f = 0; f < 2; f++)
-#pragma unroll
-        for (int m = 0; m < 4; m++) acc[f][m] = v4i{0, 0, 0, 0};
-    // what the epilogue needs is requested behind the first steps: lane l of a fragment holds row l % 16 and
-    // columns 4 (l / 16) .. +3
+
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the scales, where there are few steps
+    // lane l of a fragment holds row l % 16 and columns 4 (l / 16) .. +3
+    const uint32_t sc = (uint32_t)(uintptr_t)scales + q * 16;
     v4f sb[2], bias[2];
-    int to[4];
-    float sa[4];
-    auto request = [&]() {
 #pragma unroll
-        for (int f = 0; f < 2; f++) {
-            const int n = n0 + (SWIGLU ? 0 : 16 * f) + 4 * q;
-            const int64_t at = (int64_t)blk.e * g.N + n + (SWIGLU ? f * n_end : 0);
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                sb[f][r] = OUT != 3 && n + r < n_end ? g.sb[at + r] : 0.0f;
-                bias[f][r] = g.bias && n + r < n_end ? g.bias[at + r] : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < 4; m++) {
-            const int i = place_c(m), from = row_from(g, i, named_c[m]);
-            const bool there = blk.row + 16 * m + col < blk.end && from >= 0;
-            to[m] = there ? row_to(g, i, named_c[m]) : -1;
-            sa[m] = OUT != 3 && there ? g.sa[from] : 0.0f;
-        }
-    };
-    const int rows = blk.end - blk.row, nk = g.K_pad / 256;
-    if (rows <= 16) stream_products<1, 4>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
-    else if (rows <= 32) stream_products<2, 3>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
-    else stream_products<4, 2>(pool, wsrc, a_src, request, blk.blocks == 1, nk, wave, lane, acc);
-
+    for (int f = 0; f < 2; f++) {
+        sb[f] = __builtin_bit_cast(v4f, lds(sc + f * 64));
+        if (g.bias) bias[f] = __builtin_bit_cast(v4f, lds(sc + 256 + f * 64));
+    }
     auto scaled = [&](const v4i &t, float s, int f) {
         v4f v;
 #pragma unroll
@@ -281,12 +277,10 @@ void experts_stream_kernel(const ExpertsGemm g)
         return v;
     };
 #pragma unroll
-    for (int m = 0; m < 4; m++) {
-        if (to[m] < 0) continue;
+    for (int m = 0; m < RM; m++) {
         const int64_t row = (int64_t)to[m] * g.ldc;
         if constexpr (SWIGLU) {
             const int n = n0 + 4 * q;
-            if (n >= n_end) continue;
             const v4f a = scaled(acc[0][m] >> 4, sa[m], 0), b = scaled(acc[1][m] >> 4, sa[m], 1);
             v4f o;
 #pragma unroll
@@ -296,16 +290,32 @@ void experts_stream_kernel(const ExpertsGemm g)
                 // library: without this the compiler makes one rounding of the two (v_fma_mixlo_f16)
                 if constexpr (OUT == 1) asm("" : "+v"(o[r]));
             }
-            store4<OUT>(g.C, row + n, o, v4i{}, n_end - n, g.vec);
+            if (to[m] >= 0 && n < n_end) store4<OUT>(g.C, row + n, o, v4i{}, n_end - n, g.vec);
         } else {
 #pragma unroll
             for (int f = 0; f < 2; f++) {
                 const int n = n0 + 16 * f + 4 * q;
                 const v4i t = acc[f][m] >> 4;
-                if (n < n_end) store4<OUT>(g.C, row + n, OUT == 3 ? v4f{} : scaled(t, sa[m], f), t, n_end - n, g.vec);
+                if (to[m] >= 0 && n < n_end)
+                    store4<OUT>(g.C, row + n, OUT == 3 ? v4f{} : scaled(t, sa[m], f), t, n_end - n, g.vec);
             }
         }
     }
+}
+
+template <int OUT, bool SWIGLU>
+__global__ __launch_bounds__(64 * kWaves)
+void experts_stream_kernel(const ExpertsGemm g)
+{
+    __shared__ __attribute__((aligned(1024))) int8_t pool[kRing + kWaves * kScales];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    ExpertBlock blk;
+    if (!find_block(g.offsets, g.E, g.S, kLgRows, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
+    const Stream x{g, blk, (int)(blockIdx.x % g.n_tiles), lane, wave, pool};
+    const int rows = blk.end - blk.row;
+    if (rows <= 16) stream<OUT, SWIGLU, 1, 3>(x);
+    else if (rows <= 32) stream<OUT, SWIGLU, 2, 3>(x);
+    else stream<OUT, SWIGLU, 4, 2>(x);
 }
 
 template <int OUT, bool SWIGLU>

@@ -191,6 +191,7 @@ void experts_tile_kernel(const ExpertsGemm g)
     __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm((NSTAGE - 1) * PPW));
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     gemm::barrier();
+    asm volatile("" ::: "memory");
     constexpr int NMF = F_M * F_N;
     using C0 = std::integral_constant<int, 0>;
     using C1 = std::integral_constant<int, 1>;
@@ -214,6 +215,7 @@ void experts_tile_kernel(const ExpertsGemm g)
                     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                     __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm(PPW));
                     gemm::barrier();
+                    asm volatile("" ::: "memory");    // no read of LDS before the barrier
                     read_a(NX, 0, 0);
                     read_b(NX, 0);
                     mfmas(ks & 1, 1, NMF);
@@ -242,6 +244,7 @@ void experts_tile_kernel(const ExpertsGemm g)
     __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm(0));
     __builtin_amdgcn_s_waitcnt(gemm::waitcnt_lgkm0());
     gemm::barrier();                                  // every wave is done with the ring
+    asm volatile("" ::: "memory");
     if (wm * T_M >= rows) return;
 
     // ---- epilogue: by 32 rows, through this wave's part of the idle ring, to the rows of C ----

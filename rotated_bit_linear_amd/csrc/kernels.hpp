@@ -197,7 +197,8 @@ struct ExpertsGemm {
     int scatter;             // place i writes row rows[i], not i
     void *C;
     int64_t ldc;
-    int n_tiles, vec;        // set by the launcher
+    int n_tiles, vec;        // set by the launcher: tiles of weight rows; C's rows take stores of 4 elements
+                             // (tiles: of 16 bytes)
 };
 // the form for many rows an expert (gemm_experts_tile.hip)
 int64_t experts_tile_blocks(int64_t S, int64_t E, int64_t N);
