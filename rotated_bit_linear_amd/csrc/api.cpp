@@ -1374,18 +1374,24 @@ cr_status cr_mlp_experts_w4a8(const int8_t *a_s8, int64_t lda, const float *a_sc
     if (s != CR_OK || !any) return s;
     if ((s = current_device_ok()) != CR_OK) return s;
     const bool tp = (flags & CR_FLAG_FORCE_TWO_PASS) != 0, tr = (flags & CR_FLAG_BLOCK_TRANSPOSED) != 0;
-    if (convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) != hipSuccess)
+    // Few slots: the products sort them themselves and leave the rows between them in the slots' order; the
+    // plan would cost a launch (one token: 3.6 us of 40).  The rows are independent: the same bits.
+    const bool own_plan = S <= convrot::kOwnPlan;
+    convrot::ExpertsGemm up = experts_gemm(a_s8, lda, a_scale, T, w1, ld1, stride1, scale1, bias1, offsets, rows, S, E, 2 * F,
+                                           K_pad, top_k, own_plan, h, p.ld_h);
+    convrot::ExpertsGemm down = experts_gemm(q, p.F_pad, q_scale, S, w2, ld2, stride2, scale2, bias2, offsets, rows, S, E, N,
+                                             p.F_pad, own_plan ? 1 : 0, true, y, p.ld_y);
+    if (own_plan) {
+        up.ids = down.ids = ids;
+        up.first = down.first = (int)first;
+    } else if (convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) !=
+               hipSuccess) {
         return CR_ERR_LAUNCH;
-    if (convrot::launch_gemm_experts(experts_gemm(a_s8, lda, a_scale, T, w1, ld1, stride1, scale1, bias1, offsets, rows, S,
-                                                  E, 2 * F, K_pad, top_k, false, h, p.ld_h),
-                                     (int)dtype, true, stream) != hipSuccess)
-        return CR_ERR_LAUNCH;
+    }
+    if (convrot::launch_gemm_experts(up, (int)dtype, true, stream) != hipSuccess) return CR_ERR_LAUNCH;
     if (convrot::launch_quant_act(h, (int)dtype, p.ld_h, S, F, nullptr, q, p.F_pad, q_scale, tp, tr, stream) != hipSuccess)
         return CR_ERR_LAUNCH;
-    if (convrot::launch_gemm_experts(experts_gemm(q, p.F_pad, q_scale, S, w2, ld2, stride2, scale2, bias2, offsets, rows, S,
-                                                  E, N, p.F_pad, 0, true, y, p.ld_y),
-                                     (int)dtype, false, stream) != hipSuccess)
-        return CR_ERR_LAUNCH;
+    if (convrot::launch_gemm_experts(down, (int)dtype, false, stream) != hipSuccess) return CR_ERR_LAUNCH;
     return from_hip(convrot::launch_experts_combine(
         combine_launch(y, p.ld_y, weights, ids, T, top_k, first, E, N, residual, ld_res, out, ld_out), (int)dtype, stream));
 }

@@ -100,6 +100,7 @@ __device__ __forceinline__ void wait_first(int k)
 struct Stream {
     const ExpertsGemm &g;
     ExpertBlock blk;
+    int slots;               // without a plan: the slot of place `lane`
     int tile;                // which 128 weight rows
     int lane, wave;
     int8_t *pool;
@@ -133,8 +134,8 @@ __device__ __forceinline__ void stream(const Stream &x)
     int named_a[4], named_c[4];
 #pragma unroll
     for (int m = 0; m < RM; m++) {
-        named_a[m] = named_row(g, place_a(m));
-        named_c[m] = named_row(g, place_c(m));
+        named_a[m] = g.ids ? __shfl(x.slots, place_a(m)) : named_row(g, place_a(m));
+        named_c[m] = g.ids ? __shfl(x.slots, place_c(m)) : named_row(g, place_c(m));
     }
 
     auto weight_row = [&](int r) {                           // row r of the wave's 32
@@ -303,6 +304,31 @@ __device__ __forceinline__ void stream(const Stream &x)
     }
 }
 
+// The b-th expert among the choices of up to 64 slots, in the order of their first slots: a wave's own plan.
+// Lane p gets the slot of the expert's place p.
+__device__ __forceinline__ bool find_choice(const ExpertsGemm &g, int b, int lane, ExpertBlock &blk, int &slots)
+{
+    const uint32_t id = lane < g.S ? (uint32_t)g.ids[lane] - (uint32_t)g.first : ~0u;
+    uint64_t left = __builtin_amdgcn_ballot_w64(id < (uint32_t)g.E), mine;
+    while (true) {
+        if (left == 0) return false;
+        const uint32_t e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        mine = __builtin_amdgcn_ballot_w64(id == e);
+        if (b-- == 0) {
+            blk.e = (int)e;
+            break;
+        }
+        left &= ~mine;
+    }
+    blk.row = 0;
+    blk.end = __popcll(mine);
+    blk.blocks = 1;
+    const uint64_t below = (1ull << lane) - 1;
+    const int place = mine >> lane & 1 ? __popcll(mine & below) : blk.end + __popcll(~mine & below);
+    slots = __builtin_amdgcn_ds_permute(place << 2, lane);
+    return true;
+}
+
 template <int OUT, bool SWIGLU>
 __global__ __launch_bounds__(64 * kWaves)
 void experts_stream_kernel(const ExpertsGemm g)
@@ -310,8 +336,10 @@ void experts_stream_kernel(const ExpertsGemm g)
     __shared__ __attribute__((aligned(1024))) int8_t pool[kRing + kWaves * kScales];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     ExpertBlock blk;
-    if (!find_block(g.offsets, g.E, g.S, kLgRows, (int)(blockIdx.x / g.n_tiles), lane, blk)) return;
-    const Stream x{g, blk, (int)(blockIdx.x % g.n_tiles), lane, wave, pool};
+    const int b = (int)(blockIdx.x / g.n_tiles);
+    int slots = 0;
+    if (!(g.ids ? find_choice(g, b, lane, blk, slots) : find_block(g.offsets, g.E, g.S, kLgRows, b, lane, blk))) return;
+    const Stream x{g, blk, slots, (int)(blockIdx.x % g.n_tiles), lane, wave, pool};
     const int rows = blk.end - blk.row;
     if (rows <= 16) stream<OUT, SWIGLU, 1, 3>(x);
     else if (rows <= 32) stream<OUT, SWIGLU, 2, 3>(x);
@@ -321,7 +349,8 @@ void experts_stream_kernel(const ExpertsGemm g)
 template <int OUT, bool SWIGLU>
 hipError_t launch_stream(const ExpertsGemm &g, hipStream_t st)
 {
-    const dim3 grid((unsigned)(most_blocks(g.S, g.E, kLgRows) * g.n_tiles));
+    const int64_t blocks = g.ids ? (g.S < g.E ? g.S : g.E) : most_blocks(g.S, g.E, kLgRows);
+    const dim3 grid((unsigned)(blocks * g.n_tiles));
     hipLaunchKernelGGL((experts_stream_kernel<OUT, SWIGLU>), grid, dim3(64 * kWaves), 0, st, g);
     return hipGetLastError();
 }
@@ -341,6 +370,7 @@ int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N)
 
 hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st)
 {
+    if (g.ids && g.S > kOwnPlan) return hipErrorInvalidValue;
     if (tiled(g.S, g.E)) return launch_experts_tile(g, out_dtype, swiglu, st);
     g.n_tiles = (g.N + kTileN - 1) / kTileN;
     const int es = out_dtype < 2 ? 2 : 4;

@@ -154,6 +154,7 @@ struct AttnLaunch {
 hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st);
 
 // ---- a layer of experts (experts.hpp) ----
+constexpr int64_t kOwnPlan = 64;
 constexpr int kMostExperts = 512, kMostChoices = 32, kMostGroups = 64;
 
 struct RouteLaunch {
@@ -195,6 +196,8 @@ struct ExpertsGemm {
     int S, E, N, K_pad;
     int gather;              // 0: place i reads row i; otherwise row rows[i] / gather
     int scatter;             // place i writes row rows[i], not i
+    const int32_t *ids;      // no plan: choices of at most kOwnPlan slots, sorted by every wave for itself; the
+    int first;               // expert of weight 0
     void *C;
     int64_t ldc;
     int n_tiles, vec;        // set by the launcher: tiles of weight rows; C's rows take stores of 4 elements

@@ -70,7 +70,7 @@ class Layer:
         return out, 2.0 ** -7 * slack + half * out.norm(dim=1)
 
 
-SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 64, 512, 256, 300), (5, 2, 6, 700, 333, 90), (64, 4, 8, 256, 520, 257), (300, 3, 5, 300, 200, 64),
+SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 64, 512, 256, 300), (5, 2, 6, 700, 333, 90), (64, 1, 3, 256, 130, 70), (2, 32, 40, 300, 64, 33), (64, 4, 8, 256, 520, 257), (300, 3, 5, 300, 200, 64),
          (1100, 2, 4, 512, 256, 128)]
 
 
@@ -217,3 +217,22 @@ def test_norm_route_layer():
     off = (out.double() - total).abs()
     # FP32 sums of five terms, then half a step of bf16
     assert (off <= 2.0 ** -8 * total.abs() + 2.0 ** -20 * total.abs().max()).all(), off.max().item()
+
+
+def test_odd_choices():
+    """Repeated, negative and far choices, on a device that holds some of the experts; as the parts."""
+    for T, k in ((7, 9), (13, 5), (1, 32), (64, 1)):
+        c = Layer(T, k, 32, 256, 130, 70, seed=70 + T)
+        g = torch.Generator().manual_seed(T)
+        ids = torch.randint(-3, 42, (T, k), generator=g).int()
+        ids[0, 0], ids[-1, -1] = 2 ** 31 - 1, -2 ** 31
+        c.ids = ids.to(dev())
+        say(f"layer, odd choices, T={T} k={k}")
+        got = rbl.mlp_experts_w4a8(c.a, c.sa, c.ids, c.weights, c.w1, c.s1, c.w2, c.s2, first=4, residual=c.residual)
+        offsets, rows = rbl.experts_plan(c.ids, 32, first=4)
+        h = rbl.gemm_s8s4_experts(c.a, c.sa, c.w1, c.s1, offsets, rows, k, c.dtype, gather=True, swiglu=True,
+                                  out=torch.zeros(T * k, 136, dtype=c.dtype, device=dev())[:, :130])
+        q, s = rbl.quant_act(h, 130)
+        y = rbl.gemm_s8s4_experts(q, s, c.w2, c.s2, offsets, rows, k, c.dtype, scatter=True)
+        want = rbl.experts_combine(y, c.weights, c.ids, 32, first=4, residual=c.residual)
+        assert torch.equal(got, want)
