@@ -60,7 +60,7 @@ __device__ __forceinline__ int count_blocks(const int32_t *offsets, int E, int S
 // 0 <= row < end <= S.
 struct ExpertBlock {
     int e, row, end;         // expert, the block's first place in the order, and the end of the expert's
-    int blocks;              // blocks of the expert
+    int blocks, nth;         // blocks of the expert, and which of them this one is
 };
 __device__ __forceinline__ bool find_block(const int32_t *offsets, int E, int S, int lg, int b, int lane,
                                            ExpertBlock &out)
@@ -78,7 +78,8 @@ __device__ __forceinline__ bool find_block(const int32_t *offsets, int E, int S,
             out.end = __builtin_amdgcn_readlane(hi, l);
             out.blocks = __builtin_amdgcn_readlane(n, l);
             const int first = __builtin_amdgcn_readlane(upto, l) - out.blocks;
-            out.row = block_place(__builtin_amdgcn_readlane(lo, l), b - first, lg);
+            out.nth = b - first;
+            out.row = block_place(__builtin_amdgcn_readlane(lo, l), out.nth, lg);
             return true;
         }
         before = __builtin_amdgcn_readlane(upto, 63);

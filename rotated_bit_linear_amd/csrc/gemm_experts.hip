@@ -64,36 +64,32 @@ __device__ __forceinline__ void store4(void *C, int64_t at, const v4f &v, const 
 // of the matrix instruction, neighbouring lanes would take 16 bytes of different rows, which the texture unit
 // works off a lane's line at a time; so both operands go to LDS by direct loads in which eight (weight) and
 // sixteen (activation) lanes share a row.  A wave's weight rows are its own, the activation's are shared: one
-// barrier a step.  The ring's 72 KB let two workgroups run on a compute unit: 3 steps for up to 32 rows, 2 for
-// 64.  (One workgroup with twice the ring, or several tiles of weight rows a workgroup without a pause between
-// them: slower; 64 tokens on 64 experts, 5376 x 1792: 57 us, 110 and 59.)
+// barrier a step.  The rings' 80 KB let two workgroups run on a compute unit: three steps of weights, three of
+// the activation for up to 32 rows and two for 64, whose rows lie in L2 (48 rows an expert, 3584 x 5376: 156 us
+// with two steps of both, 151 so, 148 without conflicts of LDS banks).  Slower: one workgroup with twice the
+// ring; several tiles of weight rows a workgroup without a pause between them (64 tokens on 64 experts, 5376 x
+// 1792: 57 us, 110 and 59).
 constexpr int kWaves = 4, kTileN = 32 * kWaves, kLgRows = 6;
 constexpr int kStepW = kTileN * 128;                  // LDS bytes of a step's weight rows
-constexpr int kRing = 72 * 1024;
-constexpr int kScales = 512;                          // LDS bytes a wave: scales and biases of its weight rows
+constexpr int kRing = 80 * 1024;
 
-__device__ __forceinline__ int swz(int r) { return (r ^ (r >> 3 & 1)) & 7; }
+// Places of 16-byte chunks: those that the 16 lanes of a fragment read together cover all 64 banks.  A weight row
+// has 8 (two rows to the banks), an activation row 16.
+__device__ __forceinline__ int swz_w(int r) { return (r >> 1) & 7; }
+__device__ __forceinline__ int swz_a(int r) { return r & 15; }
 
 template <int N>
 __device__ __forceinline__ void wait_vm() { __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm(N)); }
 
-// until `steps` steps of P direct loads are left in flight, at most MOST
-template <int P, int MOST, int J = 0>
-__device__ __forceinline__ void wait_steps(int steps)
-{
-    if constexpr (J == MOST) wait_vm<J * P>();
-    else if (steps == J) wait_vm<J * P>();
-    else wait_steps<P, MOST, J + 1>(steps);
-}
-// until step k of the prologue's D - 1 is done: behind it are the prologue's later activation loads (RM a
-// step), and k steps
-template <int RM, int D, int J = 0>
+// until step k of the first DA - 1 is done: behind its activation loads are the later ones of the prologue (RM
+// a step) and k steps
+template <int RM, int DA, int J = 0>
 __device__ __forceinline__ void wait_first(int k)
 {
-    constexpr int N = (D - 2 - J) * RM + J * (4 + RM);
-    if constexpr (J == D - 2) wait_vm<N>();
+    constexpr int N = (DA - 2 - J) * RM + J * (4 + RM);
+    if constexpr (J == DA - 2) wait_vm<N>();
     else if (k == J) wait_vm<N>();
-    else wait_first<RM, D, J + 1>(k);
+    else wait_first<RM, DA, J + 1>(k);
 }
 
 // What a workgroup of the stream kernel does, the same for every number of rows.
@@ -106,19 +102,19 @@ struct Stream {
     int8_t *pool;
 };
 
-// Products of up to 16 RM rows over a ring of D steps.  Weights that nobody else reads go past the caches (64
+// Products of up to 16 RM rows over rings of DW steps of weights and DA of the activation.  Weights that nobody else reads go past the caches (64
 // tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an expert has several blocks its weights
 // come from the cache the next time (777 tokens on 60: 31 us, not 36).
-template <int OUT, bool SWIGLU, int RM, int D>
+template <int OUT, bool SWIGLU, int RM, int DW, int DA>
 __device__ __forceinline__ void stream(const Stream &x)
 {
-    constexpr int STEP = kStepW + RM * 4096, P = 4 + RM;     // LDS bytes, and direct loads a wave, of a step
-    static_assert(D * STEP <= kRing && D >= 2, "ring");
+    constexpr int kStepA = RM * 4096, RING_A = DW * kStepW;  // LDS bytes of a step's rows, and where their ring is
+    static_assert(RING_A + DA * kStepA <= kRing && DA >= 2 && DA <= 3 && (DW == DA || DW == DA + 1), "rings");
     constexpr int WC = SWIGLU ? 16 : 32;                     // columns of C a wave
     const ExpertsGemm &g = x.g;
     const ExpertBlock blk = x.blk;
     const int lane = x.lane, wave = x.wave, col = lane & 15, q = lane >> 4;
-    int8_t *const pool = x.pool, *const scales = pool + kRing + wave * kScales;
+    int8_t *const pool = x.pool;
     const int n_end = SWIGLU ? g.N >> 1 : g.N, nk = g.K_pad / 256;
     const int n0 = (x.tile * kWaves + wave) * WC;
     const bool once = blk.blocks == 1;
@@ -141,12 +137,22 @@ __device__ __forceinline__ void stream(const Stream &x)
     auto weight_row = [&](int r) {                           // row r of the wave's 32
         return SWIGLU ? min(n0 + (r & 15), n_end - 1) + (r >> 4) * n_end : min(n0 + r, n_end - 1);
     };
+    // scales and biases of the columns 4 q .. +3 of each fragment
+    v4f sb[2], bias[2];
+#pragma unroll
+    for (int f = 0; f < 2; f++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int64_t at = (int64_t)blk.e * g.N + weight_row(16 * f + 4 * q + r);
+            sb[f][r] = OUT != 3 ? g.sb[at] : 0.0f;
+            bias[f][r] = g.bias ? g.bias[at] : 0.0f;
+        }
     const int8_t *wsrc[4];                                   // where the next step lies
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const int r = 8 * j + (lane >> 3);
         wsrc[j] = reinterpret_cast<const int8_t *>(g.B) + (int64_t)blk.e * g.stride_b + (int64_t)weight_row(r) * g.ldb +
-                  (((lane & 7) ^ swz(r)) << 4);
+                  (((lane & 7) ^ swz_w(r)) << 4);
     }
     auto issue_w = [&](int at) {
 #pragma unroll
@@ -158,33 +164,26 @@ __device__ __forceinline__ void stream(const Stream &x)
         }
     };
 #pragma unroll
-    for (int s = 0; s < D - 1; s++)
-        if (s < nk) issue_w(s * STEP);
+    for (int s = 0; s < DW - 1; s++)
+        if (s < nk) issue_w(s * kStepW);
 
     const int8_t *asrc[4];
 #pragma unroll
     for (int j = 0; j < RM; j++) {
         const int r = 16 * j + 4 * wave + (lane >> 4);
-        asrc[j] = g.A + (int64_t)max(row_from(g, place_a(j), named_a[j]), 0) * g.lda + (((lane & 15) ^ swz(r)) << 4);
+        asrc[j] = g.A + (int64_t)max(row_from(g, place_a(j), named_a[j]), 0) * g.lda + (((lane & 15) ^ swz_a(r)) << 4);
     }
     auto issue_a = [&](int at) {
 #pragma unroll
         for (int j = 0; j < RM; j++) {
-            __builtin_amdgcn_global_load_lds(asrc[j], pool + at + kStepW + j * 4096 + wave * 1024, 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(asrc[j], pool + RING_A + at + j * 4096 + wave * 1024, 16, 0, 0);
             asrc[j] += 256;
         }
     };
 #pragma unroll
-    for (int s = 0; s < D - 1; s++)
-        if (s < nk) issue_a(s * STEP);
+    for (int s = 0; s < DA - 1; s++)
+        if (s < nk) issue_a(s * kStepA);
 
-    // what the epilogue needs: scales (and biases) of the weight rows, a lane each, to this wave's LDS; of the
-    // rows to registers
-    if constexpr (OUT != 3) {
-        const int64_t at = (int64_t)blk.e * g.N + weight_row(lane & 31);
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const int8_t *>(g.sb + at), scales, 4, 0, 0);
-        if (g.bias) __builtin_amdgcn_global_load_lds(reinterpret_cast<const int8_t *>(g.bias + at), scales + 256, 4, 0, 0);
-    }
     int to[4];
     float sa[4];
 #pragma unroll
@@ -201,10 +200,10 @@ __device__ __forceinline__ void stream(const Stream &x)
     uint32_t adr_w[2], adr_a[2][2];
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-        adr_w[t] = base + wave * 4096 + col * 128 + (((4 * t + q) ^ swz(col)) << 4);
+        adr_w[t] = base + wave * 4096 + col * 128 + (((4 * t + q) ^ swz_w(col)) << 4);
 #pragma unroll
         for (int h = 0; h < 2; h++)
-            adr_a[t][h] = base + kStepW + col * 256 + (((8 * t + 4 * (q >> 1) + (q & 1) + 2 * h) ^ swz(col)) << 4);
+            adr_a[t][h] = base + RING_A + col * 256 + (((8 * t + 4 * (q >> 1) + (q & 1) + 2 * h) ^ swz_a(col)) << 4);
     }
     auto lds = [](uint32_t a) { return *reinterpret_cast<const __attribute__((address_space(3))) v4i *>(a); };
     v4i acc[2][RM];
@@ -213,9 +212,9 @@ __device__ __forceinline__ void stream(const Stream &x)
 #pragma unroll
         for (int m = 0; m < RM; m++) acc[f][m] = v4i{0, 0, 0, 0};
     struct Half { v4i w[2], a[RM][2]; };
-    auto read = [&](Half &h_, uint32_t at, int t) {
+    auto read = [&](Half &h_, uint32_t at_w, uint32_t at, int t) {
 #pragma unroll
-        for (int f = 0; f < 2; f++) h_.w[f] = lds(adr_w[t] + at + f * 2048);
+        for (int f = 0; f < 2; f++) h_.w[f] = lds(adr_w[t] + at_w + f * 2048);
 #pragma unroll
         for (int m = 0; m < RM; m++)
 #pragma unroll
@@ -233,41 +232,34 @@ __device__ __forceinline__ void stream(const Stream &x)
             }
     };
 
-    // From 2 (D - 1) steps on, waits leave the steps behind the next one in flight; the loads for the epilogue
-    // in between only make the first ones wait for more.
-    const bool exact_waits = nk >= 2 * (D - 1);
-    int at = 0, ahead = (D - 1) * STEP;
+    // From 2 (DW - 1) steps on, waits leave in flight what was issued behind step k's loads; other loads in between
+    // only make the first ones wait for more.
+    const bool exact_waits = nk >= 2 * (DW - 1);
+    int at_w = 0, next_w = (DW - 1) * kStepW, at_a = 0, next_a = (DA - 1) * kStepA;
     for (int k = 0; k < nk; k++) {
         // step k's loads are done: this wave's, and behind the barrier all; and all have read step k - 1
         if (!exact_waits) wait_vm<0>();
-        else if (k < D - 1) wait_first<RM, D>(k);
-        else wait_steps<P, D - 2>(min(nk - 1 - k, D - 2));
+        else if (k < DA - 1) wait_first<RM, DA>(k);
+        else if (k + 1 < nk) wait_vm<(DA - 2) * (4 + RM) + (DW - DA) * 4>();
+        else wait_vm<0>();
         gemm::barrier();
         asm volatile("" ::: "memory");                       // no read of LDS before the barrier
         Half a, b;
-        read(a, at, 0);
-        read(b, at, 1);
-        if (k + D - 1 < nk) {
-            issue_w(ahead);
-            issue_a(ahead);
-        }
+        read(a, at_w, at_a, 0);
+        read(b, at_w, at_a, 1);
+        if (k + DA - 1 < nk) issue_a(next_a);
+        if (k + DW - 1 < nk) issue_w(next_w);
         __builtin_amdgcn_sched_barrier(0);
         multiply(a);
         multiply(b);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        at = at == (D - 1) * STEP ? 0 : at + STEP;
-        ahead = ahead == (D - 1) * STEP ? 0 : ahead + STEP;
+        at_w = at_w == (DW - 1) * kStepW ? 0 : at_w + kStepW;
+        next_w = next_w == (DW - 1) * kStepW ? 0 : next_w + kStepW;
+        at_a = at_a == (DA - 1) * kStepA ? 0 : at_a + kStepA;
+        next_a = next_a == (DA - 1) * kStepA ? 0 : next_a + kStepA;
     }
 
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");          // the scales, where there are few steps
     // lane l of a fragment holds row l % 16 and columns 4 (l / 16) .. +3
-    const uint32_t sc = (uint32_t)(uintptr_t)scales + q * 16;
-    v4f sb[2], bias[2];
-#pragma unroll
-    for (int f = 0; f < 2; f++) {
-        sb[f] = __builtin_bit_cast(v4f, lds(sc + f * 64));
-        if (g.bias) bias[f] = __builtin_bit_cast(v4f, lds(sc + 256 + f * 64));
-    }
     auto scaled = [&](const v4i &t, float s, int f) {
         v4f v;
 #pragma unroll
@@ -323,6 +315,7 @@ __device__ __forceinline__ bool find_choice(const ExpertsGemm &g, int b, int lan
     blk.row = 0;
     blk.end = __popcll(mine);
     blk.blocks = 1;
+    blk.nth = 0;
     const uint64_t below = (1ull << lane) - 1;
     const int place = mine >> lane & 1 ? __popcll(mine & below) : blk.end + __popcll(~mine & below);
     slots = __builtin_amdgcn_ds_permute(place << 2, lane);
@@ -333,17 +326,28 @@ template <int OUT, bool SWIGLU>
 __global__ __launch_bounds__(64 * kWaves)
 void experts_stream_kernel(const ExpertsGemm g)
 {
-    __shared__ __attribute__((aligned(1024))) int8_t pool[kRing + kWaves * kScales];
+    __shared__ __attribute__((aligned(1024))) int8_t pool[kRing];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     ExpertBlock blk;
     const int b = (int)(blockIdx.x / g.n_tiles);
     int slots = 0;
     if (!(g.ids ? find_choice(g, b, lane, blk, slots) : find_block(g.offsets, g.E, g.S, kLgRows, b, lane, blk))) return;
-    const Stream x{g, blk, slots, (int)(blockIdx.x % g.n_tiles), lane, wave, pool};
+    int tile = (int)(blockIdx.x % g.n_tiles);
+    if (blk.blocks > 1) {
+        // Workgroup i runs on XCD i % 8.  The blocks of an expert take a tile of its weights on the same XCD, one
+        // after another, so that all but the first find it in that XCD's cache: 8 tiles at a time, then the rest
+        // (777 tokens on 60 experts: 31.4 -> 30.2 us, 100 rows an expert: 230 -> 224).
+        const int j = blk.nth * g.n_tiles + tile, whole = g.n_tiles & ~(gemm::NUM_XCD - 1);
+        const int left = j - whole * blk.blocks, run = gemm::NUM_XCD * blk.blocks;
+        tile = left < 0 ? j / run * gemm::NUM_XCD + j % gemm::NUM_XCD : whole + left % (g.n_tiles - whole);
+        const int nth = left < 0 ? j % run / gemm::NUM_XCD : left / (g.n_tiles - whole);
+        blk.row += (nth - blk.nth) << kLgRows;
+    }
+    const Stream x{g, blk, slots, tile, lane, wave, pool};
     const int rows = blk.end - blk.row;
-    if (rows <= 16) stream<OUT, SWIGLU, 1, 3>(x);
-    else if (rows <= 32) stream<OUT, SWIGLU, 2, 3>(x);
-    else stream<OUT, SWIGLU, 4, 2>(x);
+    if (rows <= 16) stream<OUT, SWIGLU, 1, 3, 3>(x);
+    else if (rows <= 32) stream<OUT, SWIGLU, 2, 3, 3>(x);
+    else stream<OUT, SWIGLU, 4, 3, 2>(x);
 }
 
 template <int OUT, bool SWIGLU>

@@ -89,6 +89,21 @@ def test_values(T, k, E, N, K):
         Case(T, k, E, 2 * N, K, seed=10 * i + 7, bias=i == 0).check(dt, swiglu=True, scatter=i == 1)
 
 
+@pytest.mark.parametrize("steps", range(1, 10))
+def test_every_length_and_number_of_rows(steps):
+    """K of 1 to 9 blocks of 256 (the rings' depths and their ends) for experts of 1 to 150 rows."""
+    for rows in ((1, 16, 17, 32), (33, 64, 65, 150), (0, 129, 3, 200)):
+        c = Case(sum(rows), 1, 4, 150, 256 * steps, seed=60 + steps)
+        ids = torch.repeat_interleave(torch.arange(4), torch.tensor(rows))
+        ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(steps))].int()[:, None]
+        c.ids = ids.to(dev())
+        c.offsets, c.rows = ref.plan(c.ids, 4)
+        c.d_offsets = torch.tensor(c.offsets, dtype=torch.int32, device=dev())
+        c.d_rows = torch.tensor(c.rows, dtype=torch.int32, device=dev())
+        c.check(torch.int32, scatter=True)
+        c.check(torch.bfloat16, swiglu=True)
+
+
 def test_uneven_experts():
     """One expert has nearly all rows, several have none, one has a single row."""
     for skew, T in ((0.0, 500), (4.0, 500), (12.0, 300)):
