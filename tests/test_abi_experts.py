@@ -48,11 +48,11 @@ def test_plan_validation_and_workspace():
     assert plan(first=-1) == INV and plan(first=(1 << 31) - 64) == INV
     assert plan(T=1 << 28) == INV
     assert plan(ids=A16 + 2) == MIS and plan(off=A16 + 2) == MIS and plan(rows=A16 + 2) == MIS
-    assert L.cr_experts_plan_workspace_bytes(1024, 8, 64) == 0
-    need = L.cr_experts_plan_workspace_bytes(1025, 8, 64)
+    assert L.cr_experts_plan_workspace_bytes(512, 8, 64) == 0
+    need = L.cr_experts_plan_workspace_bytes(513, 8, 64)
     assert need > 0 and need % 256 == 0
-    assert plan(T=1025) == INV and plan(T=1025, ws=0x100010, wsb=1 << 30) == MIS
-    assert plan(T=1025, ws=0x100000, wsb=need - 1) == BIG
+    assert plan(T=513) == INV and plan(T=513, ws=0x100010, wsb=1 << 30) == MIS
+    assert plan(T=513, ws=0x100000, wsb=need - 1) == BIG
     assert L.cr_experts_plan_workspace_bytes(0, 8, 64) == 0 and L.cr_experts_plan_workspace_bytes(-1, 8, 64) == 0
     assert L.cr_experts_plan_workspace_bytes((1 << 31) // 8 - 1, 8, 512) <= 257 * 513 * 4
     assert L.cr_experts_plan_workspace_bytes(1 << 28, 8, 64) == 0
