@@ -559,18 +559,24 @@ def _out_rows(name, t, rows, cols, dtype=None):
         return None, cols
     if t.shape != (rows, cols) or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name} must be [{rows}, {cols}]" + (f" of {dtype}" if dtype is not None else ""))
-    return t.data_ptr(), max(_ld(t), cols)
+    ld, unit = t.stride()
+    assert unit == 1, "expected a row-major 2-D tensor (unit column stride)"
+    return t.data_ptr(), ld if ld > cols else cols
 
 
 def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags=0, stream=None):
+    _, n, k = _choices(ids, weights)
+    if n != logits.shape[0] or k != top_k:
+        raise ValueError("ids must be [T, top_k]")
+    _route(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags, stream)
+
+
+def _route(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags, stream):
     ld = _ld(logits)
     T, E = logits.shape
-    i, n, k = _choices(ids, weights)
-    if n != T or k != top_k:
-        raise ValueError("ids must be [T, top_k]")
     status = lib().cr_route_experts(
-        logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), max(ld, E), T, E, _vector("bias", bias, E), n_groups,
-        top_groups, group_sum, top_k, scale, i, weights.data_ptr(), flags, _stream(stream))
+        logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), ld if ld > E else E, T, E, _vector("bias", bias, E), n_groups,
+        top_groups, group_sum, top_k, scale, ids.data_ptr(), weights.data_ptr(), flags, _stream(stream))
     if status:
         raise CrError("cr_route_experts", status)
 
@@ -580,9 +586,15 @@ def cr_experts_plan_workspace_bytes(T, top_k, E) -> int:
 
 
 def cr_experts_plan(ids, first, E, offsets, rows, workspace=None, stream=None):
-    i, T, k = _choices(ids)
+    _, T, k = _choices(ids)
+    _vector("offsets", offsets, E + 1, torch.int32)
+    _vector("rows", rows, T * k, torch.int32)
+    _plan(ids, T, k, first, E, offsets, rows, workspace, stream)
+
+
+def _plan(ids, T, k, first, E, offsets, rows, workspace, stream):
     status = lib().cr_experts_plan(
-        i, T, k, first, E, _vector("offsets", offsets, E + 1, torch.int32), _vector("rows", rows, T * k, torch.int32),
+        ids.data_ptr(), T, k, first, E, offsets.data_ptr(), rows.data_ptr(),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, _stream(stream))
     if status:
         raise CrError("cr_experts_plan", status)
@@ -859,23 +871,24 @@ def route_experts(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = 
                   scale: float = 1.0):
     """(ids [T, top_k] int32, weights [T, top_k] fp32) of the experts that each row of logits [T, E]
     chooses, by softmax or sigmoid scores; -1 and 0 where no expert is left."""
-    T = logits.shape[0]
-    ids = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
-    weights = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
-    cr_route_experts(logits, bias, n_groups, n_groups if top_groups is None else top_groups, group_sum, top_k, scale, ids,
-                     weights, (CR_FLAG_ROUTE_SIGMOID if sigmoid else 0) | (CR_FLAG_ROUTE_RENORM if renorm else 0))
+    T, d = logits.shape[0], logits.device
+    ids = torch.empty(T, top_k, dtype=torch.int32, device=d)
+    weights = torch.empty(T, top_k, dtype=torch.float32, device=d)
+    _route(logits, bias, n_groups, n_groups if top_groups is None else top_groups, group_sum, top_k, scale, ids, weights,
+           (CR_FLAG_ROUTE_SIGMOID if sigmoid else 0) | (CR_FLAG_ROUTE_RENORM if renorm else 0), None)
     return ids, weights
 
 
 def experts_plan(ids: torch.Tensor, E: int, first: int = 0, workspace=None):
     """(offsets [E + 1] int32, rows [T * top_k] int32): the slots (choice j of token t: t * top_k + j) of
     experts first .. first + E - 1, sorted by expert; -1 behind them."""
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=ids.device)
-    rows = torch.empty(ids.numel(), dtype=torch.int32, device=ids.device)
-    if workspace is None and ids.dim() == 2:
-        need = cr_experts_plan_workspace_bytes(*ids.shape, E)
+    _, T, k = _choices(ids)
+    offsets = ids.new_empty(E + 1)
+    rows = ids.new_empty(T * k)
+    if workspace is None and T * k > 4096:            # below, none is needed
+        need = cr_experts_plan_workspace_bytes(T, k, E)
         workspace = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-    cr_experts_plan(ids, first, E, offsets, rows, workspace)
+    _plan(ids, T, k, first, E, offsets, rows, workspace, None)
     return offsets, rows
 
 

@@ -14,7 +14,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libconvrot.so")
 SOURCES = ["api.cpp", "quant_act.hip", "norm_act.hip", "rope_cache.hip", "attn_kv8.hip", "prep_weight.hip", "gemm_s8.hip", "gemm_fused.hip", "gemm_s8s4.hip", "gemm_e2m3.hip",
-           "experts.hip", "gemm_experts.hip", "gemm_experts_tile.hip"]
+           "experts.hip", "gemm_experts.hip", "gemm_experts_tile.hip",
+           "gemm_experts_row.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

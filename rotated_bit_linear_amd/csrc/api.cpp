@@ -1384,14 +1384,22 @@ cr_status cr_mlp_experts_w4a8(const int8_t *a_s8, int64_t lda, const float *a_sc
     if (own_plan) {
         up.ids = down.ids = ids;
         up.first = down.first = (int)first;
-    } else if (convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) !=
-               hipSuccess) {
-        return CR_ERR_LAUNCH;
     }
-    if (convrot::launch_gemm_experts(up, (int)dtype, true, stream) != hipSuccess) return CR_ERR_LAUNCH;
-    if (convrot::launch_quant_act(h, (int)dtype, p.ld_h, S, F, nullptr, q, p.F_pad, q_scale, tp, tr, stream) != hipSuccess)
+    if (!own_plan &&
+        convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) != hipSuccess)
         return CR_ERR_LAUNCH;
-    if (convrot::launch_gemm_experts(down, (int)dtype, false, stream) != hipSuccess) return CR_ERR_LAUNCH;
+    if (convrot::launch_gemm_experts(up, (int)dtype, true, stream) != hipSuccess) return CR_ERR_LAUNCH;
+    if (own_plan && !tr && convrot::experts_row_fits(T, p.F_pad)) {
+        // one token: the second product prepares its rows itself
+        down.A = static_cast<const int8_t *>(h);
+        down.lda = p.ld_h;
+        down.K = (int)F;
+        if (convrot::launch_experts_row(down, (int)dtype, stream) != hipSuccess) return CR_ERR_LAUNCH;
+    } else {
+        if (convrot::launch_quant_act(h, (int)dtype, p.ld_h, S, F, nullptr, q, p.F_pad, q_scale, tp, tr, stream) != hipSuccess)
+            return CR_ERR_LAUNCH;
+        if (convrot::launch_gemm_experts(down, (int)dtype, false, stream) != hipSuccess) return CR_ERR_LAUNCH;
+    }
     return from_hip(convrot::launch_experts_combine(
         combine_launch(y, p.ld_y, weights, ids, T, top_k, first, E, N, residual, ld_res, out, ld_out), (int)dtype, stream));
 }

@@ -11,53 +11,18 @@
 #include <type_traits>
 
 #include "experts.hpp"
-#include "gemm_common.hpp"
+#include "gemm_experts.hpp"
 #include "kernels.hpp"
 #include "swiglu.hpp"
 
 namespace convrot {
 namespace {
 
+using gemm::store4;
+using gemm::v4f;
 using gemm::v4i;
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ v4i widen(uint32_t d0, uint32_t d1)
-{
-    constexpr uint32_t hi = 0xF0F0F0F0u;
-    return v4i{(int32_t)((d0 << 4) & hi), (int32_t)(d0 & hi), (int32_t)((d1 << 4) & hi), (int32_t)(d1 & hi)};
-}
-
-// four neighbouring columns n .. n+3 of a row, rounded once to the output type
-template <int OUT>
-__device__ __forceinline__ void store4(void *C, int64_t at, const v4f &v, const v4i &raw, int left, bool vec)
-{
-    if constexpr (OUT == 0 || OUT == 1) {
-        uint16_t *out = static_cast<uint16_t *>(C) + at;
-        uint16_t h[4];
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            if constexpr (OUT == 0) h[r] = __bfloat16_as_ushort(__float2bfloat16(v[r]));
-            else h[r] = __half_as_ushort(__float2half(v[r]));
-        }
-        if (vec && left >= 4) {
-            *reinterpret_cast<uint2 *>(out) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-            return;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; r++)
-            if (r < left) out[r] = h[r];
-    } else {
-        uint32_t *out = static_cast<uint32_t *>(C) + at;
-        if (vec && left >= 4) {
-            if constexpr (OUT == 3) *reinterpret_cast<v4i *>(out) = raw;
-            else *reinterpret_cast<v4f *>(out) = v;
-            return;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; r++)
-            if (r < left) out[r] = OUT == 3 ? (uint32_t)raw[r] : __float_as_uint(v[r]);
-    }
-}
+using gemm::wait_vm;
+using gemm::widen;
 
 // A workgroup takes up to 64 rows of an expert and 128 weight rows, 32 a wave (with SwiGLU 16 gates and their
 // 16 values), and walks K in steps of 256 codes: whole lines of the weight.  Loaded to registers in the order
@@ -77,9 +42,6 @@ constexpr int kRing = 80 * 1024;
 // has 8 (two rows to the banks), an activation row 16.
 __device__ __forceinline__ int swz_w(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int swz_a(int r) { return r & 15; }
-
-template <int N>
-__device__ __forceinline__ void wait_vm() { __builtin_amdgcn_s_waitcnt(gemm::waitcnt_vm(N)); }
 
 // until step k of the first DA - 1 is done: behind its activation loads are the later ones of the prologue (RM
 // a step) and k steps

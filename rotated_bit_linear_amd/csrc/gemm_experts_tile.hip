@@ -11,7 +11,7 @@
 #include <type_traits>
 
 #include "experts.hpp"
-#include "gemm_common.hpp"
+#include "gemm_experts.hpp"
 #include "kernels.hpp"
 #include "swiglu.hpp"
 
@@ -19,6 +19,7 @@ namespace convrot {
 namespace {
 
 using gemm::v4i;
+using gemm::widen;
 using gemm::v16i;
 
 constexpr int W_M = 4, W_N = 2;                 // waves along M (rows), N (weight rows)
@@ -41,12 +42,6 @@ static_assert(POOL <= 160 * 1024 && NWAVE * gemm::EPI_BYTES <= MAPS, "LDS");
 
 __device__ __forceinline__ int swz_a(int r) { return (r ^ (r >> 3)) & 7; }
 __device__ __forceinline__ int swz_b(int r) { return ((r >> 1) ^ (r >> 2)) & 3; }
-
-__device__ __forceinline__ v4i widen(uint32_t d0, uint32_t d1)
-{
-    constexpr uint32_t hi = 0xF0F0F0F0u;
-    return v4i{(int32_t)((d0 << 4) & hi), (int32_t)(d0 & hi), (int32_t)((d1 << 4) & hi), (int32_t)(d1 & hi)};
-}
 
 template <int OUT>
 __device__ __forceinline__ void put4(int8_t *dst, const float (&v)[4])

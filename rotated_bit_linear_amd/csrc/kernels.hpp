@@ -198,6 +198,7 @@ struct ExpertsGemm {
     int scatter;             // place i writes row rows[i], not i
     const int32_t *ids;      // no plan: choices of at most kOwnPlan slots, sorted by every wave for itself; the
     int first;               // expert of weight 0
+    int K;                   // of the rows that launch_experts_row prepares
     void *C;
     int64_t ldc;
     int n_tiles, vec;        // set by the launcher: tiles of weight rows; C's rows take stores of 4 elements
@@ -206,6 +207,10 @@ struct ExpertsGemm {
 // the form for many rows an expert (gemm_experts_tile.hip)
 int64_t experts_tile_blocks(int64_t S, int64_t E, int64_t N);
 hipError_t launch_experts_tile(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);
+// the second product for one token (gemm_experts_row.hip): S choices `ids`, rows of C by choice; A holds rows of
+// out_dtype (lda elements, K of them) that are rotated and quantized first
+bool experts_row_fits(int64_t T, int64_t F_pad);
+hipError_t launch_experts_row(ExpertsGemm g, int out_dtype, hipStream_t st);
 // workgroups of the launch, in units of 256 threads
 int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N);
 hipError_t launch_gemm_experts(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);

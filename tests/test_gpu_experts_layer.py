@@ -70,7 +70,8 @@ class Layer:
         return out, 2.0 ** -7 * slack + half * out.norm(dim=1)
 
 
-SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 64, 512, 256, 300), (5, 2, 6, 700, 333, 90), (64, 1, 3, 256, 130, 70), (2, 32, 40, 300, 64, 33), (64, 4, 8, 256, 520, 257), (300, 3, 5, 300, 200, 64),
+SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 64, 512, 256, 300), (5, 2, 6, 700, 333, 90), (64, 1, 3, 256, 130, 70), (2, 32, 40, 300, 64, 33),
+         (1, 4, 6, 700, 1793, 90), (1, 3, 5, 1300, 4096, 140), (1, 2, 5, 256, 4100, 130), (1, 2, 3, 16500, 300, 70), (64, 4, 8, 256, 520, 257), (300, 3, 5, 300, 200, 64),
          (1100, 2, 4, 512, 256, 128)]
 
 
@@ -97,6 +98,18 @@ def test_transposed_order_of_the_second_weight():
         say(f"layer, flags {flags}")
         outs.append(c(flags=flags))
     assert torch.equal(*outs)                           # the same codes in another order: the same sums
+
+
+@pytest.mark.parametrize("T", [1, 3])
+def test_rows_between_the_products_of_every_size(T):
+    """Zero, tiny (below the codes' usual range) and large rows; one token prepares them in the second product."""
+    for scale in (0.0, 1e-38, 1e-33, 1e-20, 1.0, 1e12):
+        for dt in (torch.float32, torch.bfloat16):
+            c = Layer(T, 4, 6, 512, 700, 100, dt, seed=12, residual=False)
+            c.sa = torch.full_like(c.sa, 1e-4)
+            c.s1 = c.s1 * scale ** 0.5
+            say(f"layer T={T}, first product scaled by {scale}, {dt}")
+            assert torch.equal(c(), c.parts())
 
 
 def test_experts_dealt_out():

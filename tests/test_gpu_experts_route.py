@@ -106,8 +106,8 @@ def test_strides_and_unaligned_rows():
 
 # ------------------------------------------------------------------------------------- plan ----
 
-@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (63, 1, 5), (13, 5, 60), (128, 8, 512), (129, 8, 512), (1024, 8, 64),
-                                   (1025, 8, 64), (8193, 1, 511), (2500, 32, 256), (20000, 8, 64), (100000, 6, 8)])
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (63, 1, 5), (13, 5, 60), (128, 8, 512), (129, 8, 512), (512, 8, 64), (1024, 8, 64),
+                                   (1025, 8, 64), (4097, 1, 9), (8193, 1, 511), (2500, 32, 256), (20000, 8, 64), (100000, 6, 8)])
 def test_plan(T, k, E):
     for seed, none, first, local in ((1, 0.0, 0, E), (2, 0.3, E // 3, max(1, E // 2))):
         ids, _ = ref.random_choices(T, k, E, seed, dev(), none=none, repeats=True)
