@@ -548,8 +548,9 @@ def _expert_weight(name, w, scale, bias):
     """(address, ldb, stride, scale, bias, E, N) of a packed weight [E, N, bytes] with its scales and bias."""
     if w.dtype is not torch.uint8 or w.dim() != 3 or (w.stride(2) != 1 and w.size(2) > 1):
         raise ValueError(f"{name} must be a uint8 tensor [E, N, bytes] with contiguous rows")
-    E, N, _ = w.shape
-    return (w.data_ptr(), w.stride(1), w.stride(0), _vector(f"the scales of {name}", scale, E * N),
+    E, N, size = w.shape
+    ldb = w.stride(1) if N > 1 else size              # strides of one row, of one expert say nothing
+    return (w.data_ptr(), ldb, w.stride(0) if E > 1 else N * ldb, _vector(f"the scales of {name}", scale, E * N),
             _vector(f"the bias of {name}", bias, E * N), E, N)
 
 

@@ -238,3 +238,18 @@ def test_infinities_and_nan_reach_their_own_element():
     same = got == clean
     same[1, 5] = same[2, 9] = True
     assert same.all()
+
+
+def test_strides_of_one_expert_and_of_one_row():
+    """Views in which the stride of the axis of one says nothing: one expert of rows that lie by row first, and
+    experts of a single row each."""
+    c = Case(20, 1, 1, 64, 512, seed=90, skew=0.0)
+    by_row = torch.zeros(64, 3, 256, dtype=torch.uint8, device=dev())
+    by_row[:, 1] = c.w[0]
+    want = c.run(torch.bfloat16)
+    c.w = by_row.transpose(0, 1)[1:2]
+    assert torch.equal(c.run(torch.bfloat16), want)
+    c = Case(20, 2, 6, 1, 512, seed=91)
+    want = c.run(torch.bfloat16)
+    c.w = c.w.as_strided((6, 1, 256), (256, 16, 1))
+    assert torch.equal(c.run(torch.bfloat16), want)
