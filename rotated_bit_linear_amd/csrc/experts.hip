@@ -134,8 +134,10 @@ __device__ __forceinline__ uint64_t best_groups(const RouteLaunch &a, const F *v
         b2 = first(first(b2, o2), second(b1, o1));
         b1 = first(b1, o1);
     }
-    const F v = a.group_sum == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-    const F slack = margin * first(F(1), v < 0 ? -v : v);
+    const bool two = a.group_sum == 2 && b2 > -INFINITY;
+    const F v = two ? b1 + b2 : b1;
+    auto size_of = [&](F x) { return x < 0 ? -x : x; };
+    const F slack = margin * first(F(1), size_of(v));
     int better = 0, perhaps = 0;                      // groups that come before this one, that may
     for (int o = 0; o < a.G; o++) {
         const F w = read_lane(v, o << a.lanes_lg);
@@ -146,8 +148,13 @@ __device__ __forceinline__ uint64_t best_groups(const RouteLaunch &a, const F *v
             better += w > v || (w == v && o < g);
         }
     }
-    if constexpr (FUZZY)
-        sure = sure && __builtin_amdgcn_ballot_w64(g < a.G && perhaps >= a.top_groups && better < a.top_groups) == 0;
+    if constexpr (FUZZY) {
+        // a sum that cancels, or overflows FP32, is not as near as the margin says
+        const F part = two ? first(size_of(b1), size_of(b2)) : size_of(b1);
+        const bool far = !(part <= 2 * first(F(1), size_of(v))) || v == INFINITY;
+        sure = sure && __builtin_amdgcn_ballot_w64(
+                           g < a.G && (far || (perhaps >= a.top_groups && better < a.top_groups))) == 0;
+    }
     return __builtin_amdgcn_ballot_w64(g < a.G && better < a.top_groups);
 }
 

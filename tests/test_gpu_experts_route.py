@@ -98,6 +98,18 @@ def test_masked_infinite_and_extreme_logits(sigmoid):
         check(y, k=8, sigmoid=sigmoid)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_groups_whose_sum_cancels_or_overflows(sigmoid):
+    """Biases against which FP32 loses the scores in a group's sum, or the sum itself.  Groups' values are apart
+    by the scores' differences: far more than float64's roundings of 2^20 (2^-32) and of 1e38 (biases alone)."""
+    steps = torch.randint(0, 4, (8,), generator=torch.Generator().manual_seed(21)) / 16
+    cancel = torch.stack([torch.full((8,), 2.0 ** 20), -2.0 ** 20 + steps, torch.full((8,), -2.0 ** 21)], 1).flatten()
+    over = torch.tensor([[3.0, 2.0], [2.9, 2.9], [3.1, 0.5], [2.2, 2.1], [3.3, -1.0], [1.0, 1.0], [2.8, 2.7], [0.0, 3.2]]).flatten() * 1e38
+    for k, top in ((2, 1), (4, 3)):
+        check(logits(70, 24, 22), k=k, G=8, top_groups=top, sigmoid=sigmoid, bias=cancel)
+        check(logits(70, 16, 23), k=k, G=8, top_groups=top, sigmoid=sigmoid, bias=over)
+
+
 def test_strides_and_unaligned_rows():
     x = logits(9, 80, 12, torch.bfloat16).to(dev())
     check(x[:, 3:67], k=8)
