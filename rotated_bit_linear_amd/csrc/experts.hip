@@ -475,7 +475,8 @@ void plan_kernel(const PlanLaunch a)
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (live) a.rows[at] = bin < a.E ? (int)s : -1;
+        // within the rows even where another stream has changed the choices since they were counted
+        if (live && (uint32_t)at < (uint64_t)a.S) a.rows[at] = bin < a.E ? (int)s : -1;
     }
 }
 
