@@ -196,9 +196,9 @@ struct ExpertsGemm {
     int S, E, N, K_pad;
     int gather;              // 0: place i reads row i; otherwise row rows[i] / gather
     int scatter;             // place i writes row rows[i], not i
-    const int32_t *ids;      // no plan: choices of at most kOwnPlan slots, sorted by every wave for itself; the
-    int first;               // expert of weight 0
-    int K;                   // of the rows that launch_experts_row prepares
+    const int32_t *ids;      // instead of a plan: choices of at most kOwnPlan slots, which every wave sorts itself
+    int first;               // with ids: the expert of weight 0
+    int K;                   // columns of the rows that launch_experts_row prepares
     void *C;
     int64_t ldc;
     int n_tiles, vec;        // set by the launcher: tiles of weight rows; C's rows take stores of 4 elements
