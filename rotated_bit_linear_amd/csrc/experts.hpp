@@ -87,6 +87,18 @@ __device__ __forceinline__ bool find_block(const int32_t *offsets, int E, int S,
     return false;
 }
 
+// Tile i of an expert's blocks of rows x n_tiles columns, taken by bands of `band` blocks, each band column by
+// column.
+struct TilePlace {
+    int block, column;
+};
+__host__ __device__ inline TilePlace place_in_bands(int i, int blocks, int n_tiles, int band)
+{
+    const int nth = i / (band * n_tiles), left = blocks - nth * band, high = left < band ? left : band;
+    const int j = i - nth * band * n_tiles;
+    return {nth * band + j % high, j / high};
+}
+
 // blocks of 2^lg rows that S slots of E experts come to at most
 inline int64_t most_blocks(int64_t S, int64_t E, int lg) { return S <= E ? S : E + ((S - E) >> lg); }
 

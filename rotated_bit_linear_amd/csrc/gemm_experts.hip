@@ -321,16 +321,16 @@ hipError_t launch_stream(const ExpertsGemm &g, hipStream_t st)
     return hipGetLastError();
 }
 
-// Many rows an expert on average: 256-row tiles, whose waves share the weights in LDS.  64 experts, bf16, us
-// for 3584 x 5376 and 5376 x 1792, by streams and by tiles: 100 rows an expert 240 and 154, 280 and 161;
-// 200 rows 416 and 277, 368 and 207.
-bool tiled(int64_t S, int64_t E) { return S > 112 * E; }
+// Many rows an expert on average: 128-row tiles, whose waves share the weights in LDS.  64 experts, bf16, us
+// for 3584 x 5376 and 5376 x 1792, by streams and by tiles: 72 rows an expert 180 and 111, 204 and 111; 100
+// rows 221 and 141, 222 and 127.
+bool tiled(int64_t S, int64_t E) { return S > 88 * E; }
 
 }  // namespace
 
 int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N)
 {
-    if (tiled(S, E)) return 2 * experts_tile_blocks(S, E, N);
+    if (tiled(S, E)) return experts_tile_blocks(S, E, N);
     return most_blocks(S, E, kLgRows) * ((N + kTileN - 1) / kTileN);
 }
 

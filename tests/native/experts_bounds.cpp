@@ -50,6 +50,15 @@ int main()
         }
         if (round % 3 == 0) require(blocks <= most_blocks(S, E, lg), "more blocks than the launch has");
     }
+    for (int round = 0; round < 300; round++) {  // every tile of an expert once, in range
+        const int blocks = pick(1, 40), n_tiles = pick(1, 30), band = pick(1, 16);
+        std::vector<int> seen(blocks * n_tiles);
+        for (int i = 0; i < blocks * n_tiles; i++) {
+            const TilePlace p = place_in_bands(i, blocks, n_tiles, band);
+            require(p.block >= 0 && p.block < blocks && p.column >= 0 && p.column < n_tiles, "tile");
+            require(seen[p.block * n_tiles + p.column]++ == 0, "tile twice");
+        }
+    }
     std::printf("ok %lld\n", (long long)walked);
     return 0;
 }
