@@ -253,3 +253,37 @@ def test_strides_of_one_expert_and_of_one_row():
     want = c.run(torch.bfloat16)
     c.w = c.w.as_strided((6, 1, 256), (256, 16, 1))
     assert torch.equal(c.run(torch.bfloat16), want)
+
+
+@pytest.mark.parametrize("steps", range(1, 10))
+def test_tiles_of_every_length(steps):
+    """As above for more rows an expert on average than 88: tiles that end after 1, 64, 65 and 128 rows."""
+    for rows in ((300, 0, 193, 64), (1, 513, 128, 320)):
+        c = Case(sum(rows), 1, 4, 150, 256 * steps, seed=160 + steps, bias=True)
+        ids = torch.repeat_interleave(torch.arange(4), torch.tensor(rows))
+        c.ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(steps))].int()[:, None].to(dev())
+        c.offsets, c.rows = ref.plan(c.ids, 4)
+        c.d_offsets = torch.tensor(c.offsets, dtype=torch.int32, device=dev())
+        c.d_rows = torch.tensor(c.rows, dtype=torch.int32, device=dev())
+        bias, c.bias = c.bias, None
+        c.check(torch.int32, scatter=True)
+        c.bias = bias
+        c.check(torch.bfloat16, swiglu=True)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_more_tiles_than_run_at_once(swiglu):
+    """Each XCD has more than 64 tiles (it walks K from the end for every second 64); the dense GEMM's bits."""
+    T, k, E, N, K = 1700, 2, 3, 8300, 700
+    c = Case(T, k, E, N, K, seed=95, skew=0.5)
+    got = c.run(torch.float32, swiglu=swiglu)
+    for e in range(E):
+        at = torch.arange(c.offsets[e], c.offsets[e + 1], device=dev())
+        t = c.d_rows[at].long() // k
+        want = torch.empty(len(at), N, dtype=torch.float32, device=dev())
+        rbl.cr_gemm_s8s4_rowscale(c.a[t].contiguous(), c.sa[t].contiguous(), c.w[e], c.sw[e], want)
+        if swiglu:
+            act = torch.empty(len(at), N // 2, dtype=torch.float32, device=dev())
+            rbl.cr_swiglu(want, N // 2, act)
+            want = act
+        assert torch.equal(got[at], want)
