@@ -474,7 +474,7 @@ cr_status check_combine(const void *y, cr_dtype dt, int64_t ld_y, const float *w
 size_t plan_bytes(int64_t S, int64_t E)
 {
     int64_t runs, run;
-    convrot::plan_runs(S, runs, run);
+    convrot::plan_runs(S, E, runs, run);
     return runs > 1 ? up256((size_t)runs * (size_t)(E + 1) * 4) : 0;
 }
 

@@ -386,14 +386,32 @@ hipError_t launch_route_of(const RouteLaunch &a, hipStream_t st)
 // -------------------------------------------------------------------------------- plan ----
 
 // A stable counting sort.  A workgroup takes a run of slots, each of its waves a part of the run in
-// order; a bin more than experts takes the slots of no expert here.
+// order.  Slots of no expert here are left out, and the places behind the others' get -1; a bin more than
+// experts counts nothing and is where they begin.
 constexpr int kPlanWaves = 16;
 static_assert(kMostExperts < 64 * kPlanWaves, "a thread for each bin");
 
+// the expert of a slot, -1: none here
 __device__ __forceinline__ int bin_of(const PlanLaunch &a, int64_t slot)
 {
     const uint32_t e = (uint32_t)a.ids[slot] - (uint32_t)a.first;
-    return e < (uint32_t)a.E ? (int)e : a.E;
+    return e < (uint32_t)a.E ? (int)e : -1;
+}
+
+// Bins of the slots s, s + step, ... below `to` (kHeld of them at most; -1 behind), in one go; 0 <= s < a.S where
+// any is read.
+constexpr int kHeld = 4;
+__device__ __forceinline__ void hold_bins(const PlanLaunch &a, int64_t s, int64_t step, int64_t to, int (&bin)[kHeld])
+{
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) bin[i] = -1;
+    if (s >= to) return;
+#pragma unroll
+    for (int i = 0; i < kHeld; i++) {
+        const int64_t at = s + i * step;
+        const int b = bin_of(a, at < to ? at : s);
+        bin[i] = at < to ? b : -1;
+    }
 }
 
 // slots of each bin in each run
@@ -403,39 +421,70 @@ void plan_count_kernel(const PlanLaunch a)
     __shared__ int count[kMostExperts + 1];
     for (int i = threadIdx.x; i <= a.E; i += 64 * kPlanWaves) count[i] = 0;
     __syncthreads();
+    constexpr int64_t step = 64 * kPlanWaves;
     const int64_t from = (int64_t)blockIdx.x * a.run, to = from + a.run < a.S ? from + a.run : a.S;
-    for (int64_t s = from + threadIdx.x; s < to; s += 64 * kPlanWaves) atomicAdd(&count[bin_of(a, s)], 1);
+    for (int64_t s = from; s < to; s += kHeld * step) {
+        int bin[kHeld];
+        hold_bins(a, s + threadIdx.x, step, to, bin);
+#pragma unroll
+        for (int i = 0; i < kHeld; i++)
+            if (bin[i] >= 0) atomicAdd(&count[bin[i]], 1);
+    }
     __syncthreads();
     for (int i = threadIdx.x; i <= a.E; i += 64 * kPlanWaves) a.counts[(int64_t)blockIdx.x * (a.E + 1) + i] = count[i];
 }
 
+// Bound by chains of loads: a wave holds the bins of its first 256 slots from the count to the sort, and all
+// threads share the counts of the runs.  Both launches, 160 thousand slots on 32 of 64 experts: 12.0 -> 7.8 us,
+// half of that by leaving out the slots of no expert here, whose one bin took half of the additions; 1.6
+// million slots on 64: 21.7 -> 16.7.
 __global__ __launch_bounds__(64 * kPlanWaves)
 void plan_kernel(const PlanLaunch a)
 {
     extern __shared__ int next[];                     // [wave][bin]: its count, then where its next slot goes
-    __shared__ int sums[kPlanWaves];
+    __shared__ int named, sums[kPlanWaves], run_all[kMostExperts + 1], run_before[kMostExperts + 1];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int bins = a.E + 1;
-    for (int i = tid; i < kPlanWaves * bins; i += 64 * kPlanWaves) next[i] = 0;
-    __syncthreads();
     const int64_t part = a.run / kPlanWaves;          // a multiple of 64
     const int64_t from = (int64_t)blockIdx.x * a.run + wave * part;
-    const int64_t to = from + part < a.S ? from + part : a.S;
-    for (int64_t s = from + lane; s < to; s += 64) atomicAdd(&next[wave * bins + bin_of(a, s)], 1);
+    const int64_t to = from + part < a.S ? from + part : a.S, rest = from + kHeld * 64;
+    int held[kHeld];
+    hold_bins(a, from + lane, 64, to, held);
+    for (int i = tid; i < kPlanWaves * bins; i += 64 * kPlanWaves) next[i] = 0;
+    for (int i = tid; i < bins; i += 64 * kPlanWaves) run_all[i] = run_before[i] = 0;
+    __syncthreads();
+    if (a.runs > 1) {
+        // slots of a bin in all runs, and in the runs before this one: a group of whole waves has a thread for
+        // every bin, and the groups deal the runs out
+        const int waves = (bins + 63) >> 6, groups = kPlanWaves / waves, group = wave / waves;
+        const int bin = tid - group * waves * 64;
+        if (group < groups && bin < bins) {
+            int all = 0, before = 0;
+#pragma unroll 4
+            for (int b = group; b < (int)a.runs; b += groups) {
+                const int c = a.counts[(int64_t)b * bins + bin];
+                all += c;
+                before += b < (int)blockIdx.x ? c : 0;
+            }
+            atomicAdd(&run_all[bin], all);
+            atomicAdd(&run_before[bin], before);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; i++)
+        if (held[i] >= 0) atomicAdd(&next[wave * bins + held[i]], 1);
+    for (int64_t s = rest + lane; s < to; s += 64) {
+        const int bin = bin_of(a, s);
+        if (bin >= 0) atomicAdd(&next[wave * bins + bin], 1);
+    }
     __syncthreads();
 
-    // thread e: slots of bin e in all runs, and in the runs before this one
-    int all = 0, before = 0;
+    int all = 0;
     if (tid < bins) {
         if (a.runs == 1) {
             for (int w = 0; w < kPlanWaves; w++) all += next[w * bins + tid];
         } else {
-#pragma unroll 8
-            for (int b = 0; b < (int)a.runs; b++) {
-                const int c = a.counts[(int64_t)b * bins + tid];
-                all += c;
-                before += b < (int)blockIdx.x ? c : 0;
-            }
+            all = run_all[tid];
         }
     }
     const int upto = wave_scan(all);
@@ -444,8 +493,9 @@ void plan_kernel(const PlanLaunch a)
     int at = upto - all;
     for (int w = 0; w < wave; w++) at += sums[w];
     if (tid < bins) {
-        if (blockIdx.x == 0) a.offsets[tid] = at;     // the slots of no expert come last
-        at += before;
+        if (blockIdx.x == 0) a.offsets[tid] = at;
+        if (tid == a.E) named = at;
+        at += run_before[tid];
         for (int w = 0; w < kPlanWaves; w++) {
             const int c = next[w * bins + tid];
             next[w * bins + tid] = at;
@@ -454,10 +504,17 @@ void plan_kernel(const PlanLaunch a)
     }
     __syncthreads();
 
+#pragma unroll 1
     for (int64_t s0 = from; s0 < to; s0 += 64) {
         const int64_t s = s0 + lane;
-        const bool live = s < to;
-        const int bin = live ? bin_of(a, s) : 0;
+        int bin = held[0];
+        if (s0 < rest) {
+#pragma unroll
+            for (int i = 0; i + 1 < kHeld; i++) held[i] = held[i + 1];
+        } else {
+            bin = s < to ? bin_of(a, s) : -1;
+        }
+        const bool live = bin >= 0;
         uint64_t same = __builtin_amdgcn_ballot_w64(live);       // lanes of this lane's bin
         for (int bit = 0; bit < a.bin_bits; bit++) {
             const bool one = bin >> bit & 1;
@@ -465,7 +522,7 @@ void plan_kernel(const PlanLaunch a)
             same &= one ? ones : ~ones;
         }
         const int rank = __popcll(same & ((1ull << lane) - 1));
-        int *const place = next + wave * bins + bin;
+        int *const place = next + wave * bins + (live ? bin : 0);
         int at = 0;
         if (live) at = *place + rank;
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -476,8 +533,11 @@ void plan_kernel(const PlanLaunch a)
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         // within the rows even where another stream has changed the choices since they were counted
-        if (live && (uint32_t)at < (uint64_t)a.S) a.rows[at] = bin < a.E ? (int)s : -1;
+        if (live && (uint32_t)at < (uint64_t)a.S) a.rows[at] = (int)s;
     }
+    // behind the experts' slots: -1
+    for (int64_t s = from + lane; s < to; s += 64)
+        if (s >= named) a.rows[s] = -1;
 }
 
 // ------------------------------------------------------------------------- weighted sum ----
@@ -606,14 +666,15 @@ hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st)
     }
 }
 
-// One workgroup for 4096 slots, above runs of 1024 (8192 slots: 5.7 us, 8.7 by one workgroup) and, where the
-// counts of the runs before become the longer part, of 4096 (160 thousand slots: 9.9 us, 12.8 with 1024);
-// at most 256 runs.
-void plan_runs(int64_t S, int64_t &runs, int64_t &run)
+// One workgroup for 4096 slots, above runs of 1024 (8192 slots: 6.6 us, 8.7 by one workgroup) and, where the
+// counts of the runs before become the longer part, of 2048 for few experts (160 thousand slots, 32 experts:
+// 8.1 us, 9.1 with 4096) and of 4096 for many (512 experts: 12.9, 15.4 with 2048); at most 256 runs.
+void plan_runs(int64_t S, int64_t E, int64_t &runs, int64_t &run)
 {
     constexpr int64_t step = 64 * kPlanWaves;
     if (S < 1) S = 1;
-    runs = S <= 4096 ? 1 : S <= 65536 ? (S + 1023) / 1024 : (S + 4095) / 4096;
+    const int64_t length = S <= 65536 ? 1024 : E <= 128 ? 2048 : 4096;
+    runs = S <= 4096 ? 1 : (S + length - 1) / length;
     if (runs > 256) runs = 256;
     run = ((S + runs - 1) / runs + step - 1) / step * step;
     runs = (S + run - 1) / run;
@@ -621,7 +682,7 @@ void plan_runs(int64_t S, int64_t &runs, int64_t &run)
 
 hipError_t launch_experts_plan(PlanLaunch a, hipStream_t st)
 {
-    plan_runs(a.S, a.runs, a.run);
+    plan_runs(a.S, a.E, a.runs, a.run);
     a.bin_bits = 0;
     while ((1 << a.bin_bits) <= a.E) a.bin_bits++;
     const dim3 grid((unsigned)a.runs), threads(64 * kPlanWaves);

@@ -181,7 +181,7 @@ struct PlanLaunch {
     int64_t runs, run;       // set by the launcher: runs of `run` slots
     int bin_bits;
 };
-void plan_runs(int64_t S, int64_t &runs, int64_t &run);
+void plan_runs(int64_t S, int64_t E, int64_t &runs, int64_t &run);
 hipError_t launch_experts_plan(PlanLaunch a, hipStream_t st);
 
 struct ExpertsGemm {
