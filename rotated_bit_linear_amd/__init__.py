@@ -180,6 +180,15 @@ def _ld(t: torch.Tensor) -> int:
     return st[0]
 
 
+def _row_stride(t: torch.Tensor) -> int:
+    """Row stride of a row-major 2-D tensor, for calls that refuse one below the columns.  The stride of a
+    single row says nothing and may be anything; that of several rows is passed as it is, so that expanded
+    and overlapping rows are refused."""
+    ld = _ld(t)
+    rows, cols = t.shape
+    return cols if rows <= 1 and ld < cols else ld
+
+
 def _vector(name: str, t, n: int, dtype=torch.float32) -> int | None:
     """Address of an optional contiguous vector argument of at least n elements."""
     if t is None:
@@ -560,9 +569,7 @@ def _out_rows(name, t, rows, cols, dtype=None):
         return None, cols
     if t.shape != (rows, cols) or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name} must be [{rows}, {cols}]" + (f" of {dtype}" if dtype is not None else ""))
-    ld, unit = t.stride()
-    assert unit == 1, "expected a row-major 2-D tensor (unit column stride)"
-    return t.data_ptr(), ld if ld > cols else cols
+    return t.data_ptr(), _row_stride(t)
 
 
 def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags=0, stream=None):
@@ -573,10 +580,10 @@ def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale
 
 
 def _route(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags, stream):
-    ld = _ld(logits)
+    ld = _row_stride(logits)
     T, E = logits.shape
     status = lib().cr_route_experts(
-        logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), ld if ld > E else E, T, E, _vector("bias", bias, E), n_groups,
+        logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), ld, T, E, _vector("bias", bias, E), n_groups,
         top_groups, group_sum, top_k, scale, ids.data_ptr(), weights.data_ptr(), flags, _stream(stream))
     if status:
         raise CrError("cr_route_experts", status)
@@ -602,14 +609,14 @@ def _plan(ids, T, k, first, E, offsets, rows, workspace, stream):
 
 
 def cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, gather, c, flags=0, stream=None):
-    lda = _ld(a_s8)
+    lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
     b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias)
     S = rows.numel()
     cols = N // 2 if flags & CR_FLAG_EXPERTS_SWIGLU else N
     c_ptr, ldc = _out_rows("c", c, S, cols)
     status = lib().cr_gemm_s8s4_experts(
-        a_s8.data_ptr(), max(lda, K_pad), _vector("a_scale", a_scale, M), M, b, ldb, stride, scale, bias,
+        a_s8.data_ptr(), lda, _vector("a_scale", a_scale, M), M, b, ldb, stride, scale, bias,
         _vector("offsets", offsets, E + 1, torch.int32), _vector("rows", rows, S, torch.int32), S, E, N, K_pad, gather, c_ptr,
         _TORCH_TO_CR.get(c.dtype, -1), ldc, flags, _stream(stream))
     if status:
@@ -635,7 +642,7 @@ def cr_mlp_experts_w4a8_workspace_bytes(T, top_k, E, F, N, dtype) -> int:
 def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w2, scale2, bias2, residual, out,
                         workspace, flags=0, stream=None):
     i, T, k = _choices(ids, weights)
-    lda = _ld(a_s8)
+    lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
     p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1)
     p2, ld2, stride2, s2, b2, E2, N = _expert_weight("w2", w2, scale2, bias2)
@@ -644,7 +651,7 @@ def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w
     o, ld_out = _out_rows("out", out, T, N)
     r, ld_r = _out_rows("residual", residual, T, N, out.dtype)
     status = lib().cr_mlp_experts_w4a8(
-        a_s8.data_ptr(), max(lda, K_pad), _vector("a_scale", a_scale, T), T, K_pad, i, weights.data_ptr(), k, first, E, p1,
+        a_s8.data_ptr(), lda, _vector("a_scale", a_scale, T), T, K_pad, i, weights.data_ptr(), k, first, E, p1,
         ld1, stride1, s1, b1, rows1 // 2, p2, ld2, stride2, s2, b2, N, r, ld_r, o, _TORCH_TO_CR.get(out.dtype, -1), ld_out,
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, flags,
         _stream(stream))
