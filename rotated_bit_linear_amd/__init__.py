@@ -502,21 +502,21 @@ def cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight
                        page_table, flags=0, stream=None):
     B = _check_batch(cu_seqlens, kv_lens, page_table)
     D, Hkv = cache.D, cache.Hkv
-    ld, width = _ld(qkv), Hq * D
+    ld, width = _row_stride(qkv), Hq * D
     T, cols = qkv.shape
     if cols != width + 2 * Hkv * D:
         raise ValueError(f"qkv must hold {Hq} + 2 * {Hkv} heads of {D} elements a row")
     if q_out.dtype is not qkv.dtype or q_out.shape != (T, width):
         raise ValueError("q_out must be [T, Hq * D] of qkv's dtype")
-    ld_pos = _ld(pos)
+    ld_pos = _row_stride(pos)
     n_pos, n_axes = pos.shape
     if pos.dtype is not torch.int32 or n_pos != T:
         raise ValueError("pos must be int32 [T, axes]")
     status = lib().cr_rope_append_kv8(
         qkv.data_ptr(), _TORCH_TO_CR.get(qkv.dtype, -1), ld, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_new,
         Hq, Hkv, D, _vector("q_weight", q_weight, D), _vector("k_weight", k_weight, D), eps, pos.data_ptr(),
-        max(ld_pos, n_axes), n_axes, _vector("freq", freq, D // 2, torch.float64),
-        _vector("axis", axis, D // 2, torch.int32), q_out.data_ptr(), max(_ld(q_out), width),
+        ld_pos, n_axes, _vector("freq", freq, D // 2, torch.float64),
+        _vector("axis", axis, D // 2, torch.int32), q_out.data_ptr(), _row_stride(q_out),
         cache._with_table(page_table), flags, _stream(stream))
     if status:
         raise CrError("cr_rope_append_kv8", status)
@@ -529,13 +529,13 @@ def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
 def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm_scale, out, workspace, flags=0,
                 stream=None):
     B = _check_batch(cu_seqlens, kv_lens, page_table)
-    ld_q, shape, D = _ld(q), q.shape, cache.D
+    ld_q, shape, D = _row_stride(q), q.shape, cache.D
     T, width = shape
     if width != Hq * D or out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("q and out must be [T, Hq * D] of one dtype")
     status = lib().cr_attn_kv8(
-        q.data_ptr(), _TORCH_TO_CR.get(q.dtype, -1), max(ld_q, width), T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-        max_q, max_kv, Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), max(_ld(out), width),
+        q.data_ptr(), _TORCH_TO_CR.get(q.dtype, -1), ld_q, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(),
+        max_q, max_kv, Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), _row_stride(out),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, flags,
         _stream(stream))
     if status:

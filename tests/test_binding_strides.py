@@ -92,3 +92,39 @@ def test_experts_take_the_rows_as_they_lie(recorder):
     rbl.experts_combine(wide, WEIGHTS, IDS, E, residual=wide[:T], out=torch.zeros(T, N))
     (combine,) = (args for _, args in recorder.calls)
     assert combine[2] == N + 16 and combine[11] == N + 16 and combine[13] == N
+
+
+# ----------------------------------------------------------------------------- the cache's calls ----
+
+Hq, Hkv, D = 4, 2, 64
+CU, LENS, TABLE = torch.tensor([0, T], dtype=i32), torch.tensor([T], dtype=i32), torch.zeros(1, 1, dtype=i32)
+POS, FREQ, AXIS = torch.zeros(T, 1, dtype=i32), torch.zeros(D // 2, dtype=torch.float64), torch.zeros(D // 2, dtype=i32)
+b16 = torch.bfloat16
+
+
+def append(qkv, pos=POS, **kw):
+    cache = rbl.Kv8Cache.empty(1, Hkv, D, "cpu")
+    return rbl.rope_append_kv8(qkv, cache, CU, LENS, TABLE, T, Hq, pos, FREQ, AXIS, **kw)
+
+
+def attention(q, **kw):
+    return rbl.attn_kv8(q, rbl.Kv8Cache.empty(1, Hkv, D, "cpu"), CU, LENS, TABLE, T, T, Hq, workspace=WORKSPACE, **kw)
+
+
+@pytest.mark.parametrize("rows", [expanded, overlapping])
+def test_cache_calls_refuse_rows_that_overlap(rows):
+    qkv, q = torch.zeros(T, (Hq + 2 * Hkv) * D, dtype=b16), torch.zeros(T, Hq * D, dtype=b16)
+    refused(lambda: append(rows(T, (Hq + 2 * Hkv) * D, b16)))
+    refused(lambda: append(qkv, out=rows(T, Hq * D, b16)))
+    refused(lambda: append(qkv, pos=expanded(T, 1, i32)))
+    refused(lambda: attention(rows(T, Hq * D, b16)))
+    refused(lambda: attention(q, out=rows(T, Hq * D, b16)))
+
+
+def test_cache_calls_take_a_single_row_of_any_stride(recorder):
+    one = lambda n, dtype=b16: torch.zeros(n, dtype=dtype).as_strided((1, n), (1, 1))  # noqa: E731
+    append(one((Hq + 2 * Hkv) * D), pos=one(3, i32), out=one(Hq * D))
+    attention(one(Hq * D), out=one(Hq * D))
+    rope, attn = (args for _, args in recorder.calls)
+    assert rope[2] == (Hq + 2 * Hkv) * D and rope[15] == 3 and rope[20] == Hq * D
+    assert attn[2] == Hq * D and attn[15] == Hq * D
