@@ -553,11 +553,13 @@ def _choices(ids, weights=None):
     return ids.data_ptr(), T, k
 
 
-def _expert_weight(name, w, scale, bias):
-    """(address, ldb, stride, scale, bias, E, N) of a packed weight [E, N, bytes] with its scales and bias."""
+def _expert_weight(name, w, scale, bias, K_pad):
+    """(address, ldb, stride, scale, bias, E, N) of a packed weight [E, N, K_pad / 2] with its scales and bias."""
     if w.dtype is not torch.uint8 or w.dim() != 3 or (w.stride(2) != 1 and w.size(2) > 1):
         raise ValueError(f"{name} must be a uint8 tensor [E, N, bytes] with contiguous rows")
     E, N, size = w.shape
+    if 2 * size != K_pad:
+        raise ValueError(f"the rows of {name} must hold {K_pad} columns")
     ldb = w.stride(1) if N > 1 else size              # strides of one row, of one expert say nothing
     return (w.data_ptr(), ldb, w.stride(0) if E > 1 else N * ldb, _vector(f"the scales of {name}", scale, E * N),
             _vector(f"the bias of {name}", bias, E * N), E, N)
@@ -611,7 +613,7 @@ def _plan(ids, T, k, first, E, offsets, rows, workspace, stream):
 def cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, gather, c, flags=0, stream=None):
     lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
-    b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias)
+    b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias, K_pad)
     S = rows.numel()
     cols = N // 2 if flags & CR_FLAG_EXPERTS_SWIGLU else N
     c_ptr, ldc = _out_rows("c", c, S, cols)
@@ -644,8 +646,9 @@ def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w
     i, T, k = _choices(ids, weights)
     lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
-    p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1)
-    p2, ld2, stride2, s2, b2, E2, N = _expert_weight("w2", w2, scale2, bias2)
+    p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1, K_pad)
+    F_pad = (rows1 // 2 + 255) // 256 * 256
+    p2, ld2, stride2, s2, b2, E2, N = _expert_weight("w2", w2, scale2, bias2, F_pad)
     if M != T or E2 != E or rows1 % 2:
         raise ValueError("a_s8 must hold T rows, w1 an even number of rows, and w1 and w2 the same experts")
     o, ld_out = _out_rows("out", out, T, N)
