@@ -180,6 +180,13 @@ def _ld(t: torch.Tensor) -> int:
     return st[0]
 
 
+def _rows_s8(name: str, t: torch.Tensor):
+    """(rows, row stride) of a row-major 2-D tensor of INT8 codes, or of the same bytes."""
+    if t.dtype is not torch.int8 and t.dtype is not torch.uint8:
+        raise ValueError(f"{name} must be int8")
+    return _rows_ld(t)
+
+
 def _row_stride(t: torch.Tensor) -> int:
     """Row stride of a row-major 2-D tensor, for calls that refuse one below the columns.  The stride of a
     single row says nothing and may be anything; that of several rows is passed as it is, so that expanded
@@ -207,7 +214,7 @@ def padded_k(k: int) -> int:
 def cr_prep_weight_nvfp4(w_fp4, w_sf, global_scale, K, w_s8, w_scale, flags=0, stream=None):
     n, ld_fp4 = _rows_ld(w_fp4)
     _, ld_sf = _rows_ld(w_sf)
-    _, ld_s8 = _rows_ld(w_s8)
+    _, ld_s8 = _rows_s8("w_s8", w_s8)
     _check("cr_prep_weight_nvfp4", lib().cr_prep_weight_nvfp4(
         _ptr(w_fp4), ld_fp4, _ptr(w_sf), ld_sf, _ptr(global_scale), n, K, _ptr(w_s8), ld_s8,
         _ptr(w_scale), flags, _stream(stream)))
@@ -215,7 +222,7 @@ def cr_prep_weight_nvfp4(w_fp4, w_sf, global_scale, K, w_s8, w_scale, flags=0, s
 
 def cr_quant_act(x, K, x_s8, x_scale, flags=0, stream=None):
     M, ld_x = _rows_ld(x)
-    _, ld_s8 = _rows_ld(x_s8)
+    _, ld_s8 = _rows_s8("x_s8", x_s8)
     _check("cr_quant_act", lib().cr_quant_act(
         _ptr(x), _TORCH_TO_CR[x.dtype], ld_x, M, K, _ptr(x_s8), ld_s8, _ptr(x_scale), flags,
         _stream(stream)))
@@ -223,7 +230,7 @@ def cr_quant_act(x, K, x_s8, x_scale, flags=0, stream=None):
 
 def cr_quant_act_swiglu(h, F, x_s8, x_scale, flags=0, stream=None):
     M, ld_h = _rows_ld(h)
-    _, ld_s8 = _rows_ld(x_s8)
+    _, ld_s8 = _rows_s8("x_s8", x_s8)
     _check("cr_quant_act_swiglu", lib().cr_quant_act_swiglu(
         _ptr(h), _TORCH_TO_CR[h.dtype], ld_h, M, F, _ptr(x_s8), ld_s8, _ptr(x_scale), flags,
         _stream(stream)))
@@ -231,7 +238,7 @@ def cr_quant_act_swiglu(h, F, x_s8, x_scale, flags=0, stream=None):
 
 def cr_quant_act_ex(x, K, swiglu, pre_scale, x_s8, x_scale, flags=0, stream=None):
     M, ld_x = _rows_ld(x)
-    _, ld_s8 = _rows_ld(x_s8)
+    _, ld_s8 = _rows_s8("x_s8", x_s8)
     _check("cr_quant_act_ex", lib().cr_quant_act_ex(
         _ptr(x), _TORCH_TO_CR[x.dtype], ld_x, int(bool(swiglu)), M, K, _ptr(pre_scale), _ptr(x_s8), ld_s8,
         _ptr(x_scale), flags, _stream(stream)))
@@ -239,6 +246,7 @@ def cr_quant_act_ex(x, K, swiglu, pre_scale, x_s8, x_scale, flags=0, stream=None
 
 def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=0, stream=None):
     M, ld_x = _rows_ld(x)
+    _, ld_s8 = _rows_s8("x_s8", x_s8)
     r = h = None
     ld_r = ld_h = 0
     if residual is not None:
@@ -251,7 +259,7 @@ def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=
         h, ld_h = sum.data_ptr(), _ld(sum)
     status = lib().cr_quant_act_rmsnorm(
         x.data_ptr(), _TORCH_TO_CR.get(x.dtype, -1), ld_x, r, ld_r, h, ld_h, _vector("weight", weight, K), eps, M, K,
-        x_s8.data_ptr(), _ld(x_s8), x_scale.data_ptr(), flags, _stream(stream))
+        x_s8.data_ptr(), ld_s8, x_scale.data_ptr(), flags, _stream(stream))
     if status:
         raise CrError("cr_quant_act_rmsnorm", status)
 
@@ -264,8 +272,8 @@ def cr_swiglu(h, F, out, stream=None):
 
 
 def cr_gemm_s8_rowscale(a_s8, a_scale, b_s8, b_scale, c, stream=None, M=None, N=None):
-    Ma, lda = _rows_ld(a_s8)
-    Nb, ldb = _rows_ld(b_s8)
+    Ma, lda = _rows_s8("a_s8", a_s8)
+    Nb, ldb = _rows_s8("b_s8", b_s8)
     _, ldc = _rows_ld(c)
     M = Ma if M is None else M
     N = Nb if N is None else N
@@ -280,8 +288,8 @@ def cr_linear_nvfp4_workspace_bytes(M, N, K, max_tile_bytes=0) -> int:
 
 
 def cr_gemm_s8_rowscale_bias(a_s8, a_scale, b_s8, b_scale, bias, c, stream=None):
-    M, lda = _rows_ld(a_s8)
-    N, ldb = _rows_ld(b_s8)
+    M, lda = _rows_s8("a_s8", a_s8)
+    N, ldb = _rows_s8("b_s8", b_s8)
     _, ldc = _rows_ld(c)
     _check("cr_gemm_s8_rowscale_bias", lib().cr_gemm_s8_rowscale_bias(
         _ptr(a_s8), lda, _ptr(a_scale), _ptr(b_s8), ldb, _ptr(b_scale), _ptr(bias), M, N, a_s8.shape[1],
@@ -338,7 +346,7 @@ def cr_weight_amax_nvfp4(w_fp4, w_sf, global_scale, K, w_amax, flags=0, stream=N
 
 def cr_gemm_nvfp4_fused(a_s8, a_scale, w_fp4, w_sf, global_scale, w_amax, K, c, bias=None, flags=0,
                         stream=None):
-    M, lda = _rows_ld(a_s8)
+    M, lda = _rows_s8("a_s8", a_s8)
     N, ld_fp4 = _rows_ld(w_fp4)
     _, ld_sf = _rows_ld(w_sf)
     _, ldc = _rows_ld(c)
@@ -355,7 +363,7 @@ def cr_quant_weight_w4(w, K, w_s4, w_scale, flags=0, stream=None):
 
 
 def cr_gemm_s8s4_rowscale(a_s8, a_scale, b_s4, b_scale, c, bias=None, stream=None):
-    M, lda = _rows_ld(a_s8)
+    M, lda = _rows_s8("a_s8", a_s8)
     N, ldb = _rows_ld(b_s4)
     _, ldc = _rows_ld(c)
     _check("cr_gemm_s8s4_rowscale", lib().cr_gemm_s8s4_rowscale(
@@ -611,6 +619,8 @@ def _plan(ids, T, k, first, E, offsets, rows, workspace, stream):
 
 
 def cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, gather, c, flags=0, stream=None):
+    if a_s8.dtype is not torch.int8:
+        raise ValueError("a_s8 must be int8")
     lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
     b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias, K_pad)
@@ -644,6 +654,8 @@ def cr_mlp_experts_w4a8_workspace_bytes(T, top_k, E, F, N, dtype) -> int:
 def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w2, scale2, bias2, residual, out,
                         workspace, flags=0, stream=None):
     i, T, k = _choices(ids, weights)
+    if a_s8.dtype is not torch.int8:
+        raise ValueError("a_s8 must be int8")
     lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
     p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1, K_pad)
