@@ -1389,7 +1389,7 @@ cr_status cr_mlp_experts_w4a8(const int8_t *a_s8, int64_t lda, const float *a_sc
         convrot::launch_experts_plan(plan_launch(ids, S, first, E, offsets, rows, at(p.off_counts)), stream) != hipSuccess)
         return CR_ERR_LAUNCH;
     if (convrot::launch_gemm_experts(up, (int)dtype, true, stream) != hipSuccess) return CR_ERR_LAUNCH;
-    if (own_plan && !tr && convrot::experts_row_fits(T, p.F_pad)) {
+    if (own_plan && !tr && convrot::experts_row_fits(T, S, N, p.F_pad)) {
         // one token: the second product prepares its rows itself
         down.A = static_cast<const int8_t *>(h);
         down.lda = p.ld_h;

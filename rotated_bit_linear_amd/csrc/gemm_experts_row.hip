@@ -25,8 +25,10 @@ using gemm::wait_vm;
 using gemm::widen;
 
 constexpr int kWaves = 4, kTileN = 32 * kWaves;
+static_assert(kTileN == kRowTile, "the launch's count of workgroups");
 constexpr int kStep = kTileN * 128, kDepth = 3;       // LDS bytes of a step of 256 columns, steps of the ring
 constexpr int kMostEach = 4, kMostCodes = 256 * kWaves * kMostEach;   // blocks of 256 a wave prepares; columns
+static_assert(kMostCodes == kRowMostCodes, "the longest row");
 
 __device__ __forceinline__ int swz_w(int r) { return (r >> 1) & 7; }
 
@@ -221,8 +223,6 @@ hipError_t launch_row_of(const ExpertsGemm &g, hipStream_t st)
 }
 
 }  // namespace
-
-bool experts_row_fits(int64_t T, int64_t F_pad) { return T == 1 && F_pad <= kMostCodes; }
 
 hipError_t launch_experts_row(ExpertsGemm g, int out_dtype, hipStream_t st)
 {

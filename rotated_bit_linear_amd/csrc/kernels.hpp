@@ -208,8 +208,15 @@ struct ExpertsGemm {
 int64_t experts_tile_blocks(int64_t S, int64_t E, int64_t N);
 hipError_t launch_experts_tile(ExpertsGemm g, int out_dtype, bool swiglu, hipStream_t st);
 // the second product for one token (gemm_experts_row.hip): S choices `ids`, rows of C by choice; A holds rows of
-// out_dtype (lda elements, K of them) that are rotated and quantized first
-bool experts_row_fits(int64_t T, int64_t F_pad);
+// out_dtype (lda elements, K of them) that are rotated and quantized first.  A workgroup takes one choice and
+// kRowTile weight rows; the codes of its row lie in LDS, and their values in the registers of the waves that
+// prepare them: up to kRowMostCodes.  Every choice has workgroups, a repeated one too, so there may be more than
+// a dispatch counts where the stream kernel's, one set an expert, are fewer: then that one does it.
+constexpr int kRowTile = 128, kRowMostCodes = 4096;
+inline bool experts_row_fits(int64_t T, int64_t S, int64_t N, int64_t F_pad)
+{
+    return T == 1 && F_pad <= kRowMostCodes && S * ((N + kRowTile - 1) / kRowTile) <= kMostBlocks;
+}
 hipError_t launch_experts_row(ExpertsGemm g, int out_dtype, hipStream_t st);
 // workgroups of the launch, in units of 256 threads
 int64_t experts_gemm_blocks(int64_t S, int64_t E, int64_t N);
