@@ -66,13 +66,16 @@ __device__ __forceinline__ double read_lane(double v, int lane)
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
     return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
 }
-// 1 / d for d >= 1, infinite d included: the instruction's estimate and two Newton steps, within 2^-51
-__device__ __forceinline__ double recip_f64(double d)
+// 1 / (1 + exp(-x)) in FP64: the instruction's estimate of the reciprocal and two Newton steps, within 2^-51.
+// The denominator is held times 2^-60, so that it, its reciprocal and their products are normal numbers up to the
+// exponential's overflow (x of -709.78; 0 from there on); the factor is exact, but for scores below the normal range.
+__device__ __forceinline__ double sigmoid_f64(float x)
 {
+    const double d = fma(exp(-(double)x), 0x1p-60, 0x1p-60);
     double y = __builtin_amdgcn_rcp(d);
     y = fma(fma(-d, y, 1.0), y, y);
     y = fma(fma(-d, y, 1.0), y, y);
-    return d < 0x1p1000 ? y : 0.0;
+    return d < INFINITY ? y * 0x1p-60 : 0.0;
 }
 
 // One wave a token; lane l holds experts l, l + 64, ...
@@ -199,7 +202,6 @@ void route_kernel(const RouteLaunch a)
     auto valid = [&](int i, auto v) { return l[i] > -INFINITY && v > -INFINITY; };
     // exp(l - most), 1 where they are equal (infinite or not)
     auto power = [&](float x) { return x == most ? 1.0 : exp((double)x - (double)most); };
-    auto sigmoid = [&](float x) { return recip_f64(1.0 + exp(-(double)x)); };
 
     bool sure = true;
     float value[NE];
@@ -314,7 +316,7 @@ void route_kernel(const RouteLaunch a)
         double exact[NE];
 #pragma unroll
         for (int i = 0; i < NE; i++) {
-            exact[i] = (a.sigmoid ? sigmoid(l[i]) : power(l[i]) * norm) + (double)b[i];
+            exact[i] = (a.sigmoid ? sigmoid_f64(l[i]) : power(l[i]) * norm) + (double)b[i];
             const double v = a.bias ? exact[i] : (double)l[i];
             const uint64_t k = ordered(v);
             hi[i] = valid(i, v) ? (uint32_t)(k >> 32) : 0u;           // a number's upper half is not 0
@@ -359,7 +361,7 @@ void route_kernel(const RouteLaunch a)
     }
     // the chosen experts' own scores, a lane each
     const float chosen = id < 0 ? 0.0f : Elem<DT>::cvt(row[id]);
-    const double s = id < 0 ? 0.0 : a.sigmoid ? sigmoid(chosen) : power(chosen) * norm;
+    const double s = id < 0 ? 0.0 : a.sigmoid ? sigmoid_f64(chosen) : power(chosen) * norm;
     double w = s * (double)a.scale;
     if (a.renorm) {
         const double sum = wave_sum(s);
