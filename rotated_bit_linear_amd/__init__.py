@@ -182,18 +182,20 @@ def _ld(t: torch.Tensor) -> int:
 
 def _rows_s8(name: str, t: torch.Tensor):
     """(rows, row stride) of a row-major 2-D tensor of INT8 codes, or of the same bytes."""
-    if t.dtype is not torch.int8 and t.dtype is not torch.uint8:
+    dtype, st = t.dtype, t.stride()
+    if dtype is not torch.int8 and dtype is not torch.uint8:
         raise ValueError(f"{name} must be int8")
-    return _rows_ld(t)
+    assert len(st) == 2 and st[1] == 1, "expected a row-major 2-D tensor (unit column stride)"
+    return t.size(0), st[0]
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """Row stride of a row-major 2-D tensor, for calls that refuse one below the columns.  The stride of a
-    single row says nothing and may be anything; that of several rows is passed as it is, so that expanded
+def _row_stride(t: torch.Tensor, rows: int, cols: int) -> int:
+    """Row stride of a row-major tensor [rows, cols], for calls that refuse one below the columns.  The stride
+    of a single row says nothing and may be anything; that of several rows is passed as it is, so that expanded
     and overlapping rows are refused."""
-    ld = _ld(t)
-    rows, cols = t.shape
-    return cols if rows <= 1 and ld < cols else ld
+    ld, unit = t.stride()
+    assert unit == 1, "expected a row-major 2-D tensor (unit column stride)"
+    return cols if ld < cols and rows < 2 else ld
 
 
 def _vector(name: str, t, n: int, dtype=torch.float32) -> int | None:
@@ -246,7 +248,9 @@ def cr_quant_act_ex(x, K, swiglu, pre_scale, x_s8, x_scale, flags=0, stream=None
 
 def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=0, stream=None):
     M, ld_x = _rows_ld(x)
-    _, ld_s8 = _rows_s8("x_s8", x_s8)
+    dtype = x_s8.dtype
+    if dtype is not torch.int8 and dtype is not torch.uint8:
+        raise ValueError("x_s8 must be int8")
     r = h = None
     ld_r = ld_h = 0
     if residual is not None:
@@ -259,7 +263,7 @@ def cr_quant_act_rmsnorm(x, residual, sum, weight, eps, K, x_s8, x_scale, flags=
         h, ld_h = sum.data_ptr(), _ld(sum)
     status = lib().cr_quant_act_rmsnorm(
         x.data_ptr(), _TORCH_TO_CR.get(x.dtype, -1), ld_x, r, ld_r, h, ld_h, _vector("weight", weight, K), eps, M, K,
-        x_s8.data_ptr(), ld_s8, x_scale.data_ptr(), flags, _stream(stream))
+        x_s8.data_ptr(), _ld(x_s8), x_scale.data_ptr(), flags, _stream(stream))
     if status:
         raise CrError("cr_quant_act_rmsnorm", status)
 
@@ -510,21 +514,21 @@ def cr_rope_append_kv8(qkv, cu_seqlens, kv_lens, max_new, Hq, q_weight, k_weight
                        page_table, flags=0, stream=None):
     B = _check_batch(cu_seqlens, kv_lens, page_table)
     D, Hkv = cache.D, cache.Hkv
-    ld, width = _row_stride(qkv), Hq * D
     T, cols = qkv.shape
+    ld, width = _row_stride(qkv, T, cols), Hq * D
     if cols != width + 2 * Hkv * D:
         raise ValueError(f"qkv must hold {Hq} + 2 * {Hkv} heads of {D} elements a row")
     if q_out.dtype is not qkv.dtype or q_out.shape != (T, width):
         raise ValueError("q_out must be [T, Hq * D] of qkv's dtype")
-    ld_pos = _row_stride(pos)
     n_pos, n_axes = pos.shape
+    ld_pos = _row_stride(pos, n_pos, n_axes)
     if pos.dtype is not torch.int32 or n_pos != T:
         raise ValueError("pos must be int32 [T, axes]")
     status = lib().cr_rope_append_kv8(
         qkv.data_ptr(), _TORCH_TO_CR.get(qkv.dtype, -1), ld, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(), max_new,
         Hq, Hkv, D, _vector("q_weight", q_weight, D), _vector("k_weight", k_weight, D), eps, pos.data_ptr(),
         ld_pos, n_axes, _vector("freq", freq, D // 2, torch.float64),
-        _vector("axis", axis, D // 2, torch.int32), q_out.data_ptr(), _row_stride(q_out),
+        _vector("axis", axis, D // 2, torch.int32), q_out.data_ptr(), _row_stride(q_out, T, width),
         cache._with_table(page_table), flags, _stream(stream))
     if status:
         raise CrError("cr_rope_append_kv8", status)
@@ -537,13 +541,14 @@ def cr_attn_kv8_workspace_bytes(T, B, max_q, max_kv, Hq, Hkv, D) -> int:
 def cr_attn_kv8(q, cu_seqlens, kv_lens, max_q, max_kv, Hq, cache, page_table, sm_scale, out, workspace, flags=0,
                 stream=None):
     B = _check_batch(cu_seqlens, kv_lens, page_table)
-    ld_q, shape, D = _row_stride(q), q.shape, cache.D
+    shape, D = q.shape, cache.D
     T, width = shape
+    ld_q = _row_stride(q, T, width)
     if width != Hq * D or out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("q and out must be [T, Hq * D] of one dtype")
     status = lib().cr_attn_kv8(
         q.data_ptr(), _TORCH_TO_CR.get(q.dtype, -1), ld_q, T, B, cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-        max_q, max_kv, Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), _row_stride(out),
+        max_q, max_kv, Hq, cache.Hkv, D, cache._with_table(page_table), sm_scale, out.data_ptr(), _row_stride(out, T, width),
         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, flags,
         _stream(stream))
     if status:
@@ -579,7 +584,7 @@ def _out_rows(name, t, rows, cols, dtype=None):
         return None, cols
     if t.shape != (rows, cols) or (dtype is not None and t.dtype is not dtype):
         raise ValueError(f"{name} must be [{rows}, {cols}]" + (f" of {dtype}" if dtype is not None else ""))
-    return t.data_ptr(), _row_stride(t)
+    return t.data_ptr(), _row_stride(t, rows, cols)
 
 
 def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags=0, stream=None):
@@ -590,8 +595,8 @@ def cr_route_experts(logits, bias, n_groups, top_groups, group_sum, top_k, scale
 
 
 def _route(logits, bias, n_groups, top_groups, group_sum, top_k, scale, ids, weights, flags, stream):
-    ld = _row_stride(logits)
     T, E = logits.shape
+    ld = _row_stride(logits, T, E)
     status = lib().cr_route_experts(
         logits.data_ptr(), _TORCH_TO_CR.get(logits.dtype, -1), ld, T, E, _vector("bias", bias, E), n_groups,
         top_groups, group_sum, top_k, scale, ids.data_ptr(), weights.data_ptr(), flags, _stream(stream))
@@ -621,8 +626,8 @@ def _plan(ids, T, k, first, E, offsets, rows, workspace, stream):
 def cr_gemm_s8s4_experts(a_s8, a_scale, b_s4, b_scale, bias, offsets, rows, gather, c, flags=0, stream=None):
     if a_s8.dtype is not torch.int8:
         raise ValueError("a_s8 must be int8")
-    lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
+    lda = _row_stride(a_s8, M, K_pad)
     b, ldb, stride, scale, bias, E, N = _expert_weight("b_s4", b_s4, b_scale, bias, K_pad)
     S = rows.numel()
     cols = N // 2 if flags & CR_FLAG_EXPERTS_SWIGLU else N
@@ -656,8 +661,8 @@ def cr_mlp_experts_w4a8(a_s8, a_scale, ids, weights, first, w1, scale1, bias1, w
     i, T, k = _choices(ids, weights)
     if a_s8.dtype is not torch.int8:
         raise ValueError("a_s8 must be int8")
-    lda = _row_stride(a_s8)
     M, K_pad = a_s8.shape
+    lda = _row_stride(a_s8, M, K_pad)
     p1, ld1, stride1, s1, b1, E, rows1 = _expert_weight("w1", w1, scale1, bias1, K_pad)
     F_pad = (rows1 // 2 + 255) // 256 * 256
     p2, ld2, stride2, s2, b2, E2, N = _expert_weight("w2", w2, scale2, bias2, F_pad)
