@@ -623,6 +623,7 @@ cr_status cr_attn_kv8(const void *q, cr_dtype dtype, int64_t ld_q, int64_t T, in
 #define CR_MAX_EXPERTS 512
 #define CR_MAX_CHOICES 32
 #define CR_MAX_EXPERT_GROUPS 64
+#define CR_PLAN_SLOTS_IN_PLACE 4096 /* cr_experts_plan needs no workspace up to here */
 
 /*
  * Router: the top_k experts of each token and their weights.

@@ -402,7 +402,7 @@ bool attn_plan(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t Hq, 
 // ---- a layer of experts ----
 
 static_assert(CR_MAX_EXPERTS == convrot::kMostExperts && CR_MAX_CHOICES == convrot::kMostChoices &&
-              CR_MAX_EXPERT_GROUPS == convrot::kMostGroups, "limits of the header and the kernels");
+              CR_MAX_EXPERT_GROUPS == convrot::kMostGroups && CR_PLAN_SLOTS_IN_PLACE == convrot::kOneRun, "limits of the header and the kernels");
 
 // tokens, choices and the experts here
 cr_status check_slots(int64_t T, int64_t top_k, int64_t first, int64_t E)

@@ -668,7 +668,7 @@ hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st)
     }
 }
 
-// One workgroup for 4096 slots, above runs of 1024 (8192 slots: 6.6 us, 8.7 by one workgroup) and, where the
+// One workgroup up to 4096 slots, above runs of 1024 (8192 slots: 6.6 us, 8.7 by one workgroup) and, where the
 // counts of the runs before become the longer part, of 2048 for few experts (160 thousand slots, 32 experts:
 // 8.1 us, 9.1 with 4096) and of 4096 for many (512 experts: 12.9, 15.4 with 2048); at most 256 runs.
 void plan_runs(int64_t S, int64_t E, int64_t &runs, int64_t &run)
@@ -676,7 +676,7 @@ void plan_runs(int64_t S, int64_t E, int64_t &runs, int64_t &run)
     constexpr int64_t step = 64 * kPlanWaves;
     if (S < 1) S = 1;
     const int64_t length = S <= 65536 ? 1024 : E <= 128 ? 2048 : 4096;
-    runs = S <= 4096 ? 1 : (S + length - 1) / length;
+    runs = S <= kOneRun ? 1 : (S + length - 1) / length;
     if (runs > 256) runs = 256;
     run = ((S + runs - 1) / runs + step - 1) / step * step;
     runs = (S + run - 1) / run;

@@ -156,6 +156,7 @@ hipError_t launch_attn_kv8(const AttnLaunch &l, hipStream_t st);
 // ---- a layer of experts (experts.hpp) ----
 constexpr int64_t kOwnPlan = 64;
 constexpr int kMostExperts = 512, kMostChoices = 32, kMostGroups = 64;
+constexpr int64_t kOneRun = 4096;   // slots that the plan sorts in one workgroup, without a workspace
 
 struct RouteLaunch {
     const void *logits;
