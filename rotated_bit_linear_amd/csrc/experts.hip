@@ -550,7 +550,8 @@ template <> __device__ __forceinline__ uint32_t round_to<1>(float v) { return __
 template <> __device__ __forceinline__ uint32_t round_to<2>(float v) { return __float_as_uint(v); }
 
 // 16 bytes of a row in one access, wherever the row begins: rows are element-aligned, and the hardware takes
-// such an access at any address.  Elements past the row's end are neither read nor written.
+// such an access at any address.  Elements past the row's end are neither read nor written.  PAST: read past the
+// caches; chosen when the kernel is compiled, because the compiler makes one plain load of a choice at run time.
 template <int DT>
 struct Piece {
     typedef typename Elem<DT>::T T;
@@ -558,11 +559,12 @@ struct Piece {
     typedef T Vec __attribute__((ext_vector_type(V)));
     typedef Vec Loose __attribute__((aligned(sizeof(T))));
     T e[V];
-    __device__ __forceinline__ void load(const T *p, int left, bool past)
+    template <bool PAST>
+    __device__ __forceinline__ void load(const T *p, int left)
     {
         if (left >= V) {
             Vec v;
-            if (past) v = __builtin_nontemporal_load(reinterpret_cast<const Loose *>(p));
+            if constexpr (PAST) v = __builtin_nontemporal_load(reinterpret_cast<const Loose *>(p));
             else v = *reinterpret_cast<const Loose *>(p);
 #pragma unroll
             for (int i = 0; i < V; i++) e[i] = v[i];
@@ -587,12 +589,13 @@ struct Piece {
 };
 
 // A wave takes 64 pieces of 16 bytes of one token's row; the rows of up to kAhead choices are requested
-// before the first is used.  Rows that the last cache does not hold are read past the caches (3000 tokens, 8 rows
-// of 4096 FP32: 85 -> 74 us), others may still lie there (64 tokens: 4.4 us, not 5.5).  Bound by HBM: 19989
-// tokens, 8 rows of 5376 bf16 with a residual 384 us, 5.6 TB/s.
+// before the first is used.  Rows that the last cache does not hold are read past the caches (8 rows a token, just
+// written: 3000 tokens of 4096 FP32 88 -> 62 us, 6000 of 5376 bf16 126 -> 112, 19989 391 -> 387), others may still
+// lie there (1500 tokens of 4096 FP32: 25.8 us, 26.6 past the caches; 512 of 5376 bf16 11.0 and 11.6).  Bound by
+// HBM: 19989 tokens, 8 rows of 5376 bf16 with a residual 384 us on the same rows again, 5.6 TB/s.
 constexpr int kCombineWaves = 4, kAhead = 8;
 
-template <int DT>
+template <int DT, bool PAST>
 __global__ __launch_bounds__(64 * kCombineWaves)
 void combine_kernel(const CombineLaunch a)
 {
@@ -612,14 +615,14 @@ void combine_kernel(const CombineLaunch a)
     const float *weights = a.weights + t * a.k;
     const T *y = static_cast<const T *>(a.y) + t * a.k * a.ld_y + n;
     P res;
-    if (a.residual) res.load(static_cast<const T *>(a.residual) + t * a.ld_res + n, left, false);
+    if (a.residual) res.template load<false>(static_cast<const T *>(a.residual) + t * a.ld_res + n, left);
     for (int j0 = 0; j0 < a.k; j0 += kAhead) {
         P p[kAhead];
         bool here[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; j++) {
             here[j] = j0 + j < a.k && (uint32_t)ids[j0 + j] - (uint32_t)a.first < (uint32_t)a.E;
-            if (here[j]) p[j].load(y + (j0 + j) * a.ld_y, left, a.past);
+            if (here[j]) p[j].template load<PAST>(y + (j0 + j) * a.ld_y, left);
         }
 #pragma unroll
         for (int j = 0; j < kAhead; j++)
@@ -645,10 +648,11 @@ hipError_t launch_combine_of(CombineLaunch a, hipStream_t st)
 {
     constexpr int cols = 64 * Piece<DT>::V;
     a.pieces = (a.N + cols - 1) / cols;
-    a.past = a.T * a.k > (int64_t)(256 << 20) / (int64_t)sizeof(typename Elem<DT>::T) / a.N;
+    const bool past = a.T * a.k > (int64_t)(256 << 20) / (int64_t)sizeof(typename Elem<DT>::T) / a.N;
     const int64_t waves = a.T * a.pieces;
-    hipLaunchKernelGGL((combine_kernel<DT>), dim3((unsigned)((waves + kCombineWaves - 1) / kCombineWaves)),
-                       dim3(64 * kCombineWaves), 0, st, a);
+    const dim3 grid((unsigned)((waves + kCombineWaves - 1) / kCombineWaves)), threads(64 * kCombineWaves);
+    if (past) hipLaunchKernelGGL((combine_kernel<DT, true>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((combine_kernel<DT, false>), grid, threads, 0, st, a);
     return hipGetLastError();
 }
 

@@ -233,7 +233,7 @@ struct CombineLaunch {
     int64_t ld_res;
     void *out;
     int64_t ld_out;
-    int pieces, past;        // set by the launcher: waves a token, y past the caches
+    int pieces;              // set by the launcher: waves a token
 };
 hipError_t launch_experts_combine(const CombineLaunch &a, int dtype, hipStream_t st);
 
