@@ -88,7 +88,7 @@ __device__ __forceinline__ double sigmoid_f64(float x)
 // softmax: a sum of up to 512 powers in 14 levels, 2^-20; the bias' addition 2^-24.)
 // The choice: each lane sorts its own keys, then k times the wave's largest head, the lowest expert where
 // several have it, is taken.  Bound by its instructions: 19989 tokens, 256 experts in 8 groups, sigmoid with a
-// bias, 8 choices 27 us (42 wholly in FP64); 64 experts, softmax 12.
+// bias, 8 choices 28 us in a captured loop (the first form, wholly in FP64, 42); 64 experts, softmax 12.
 constexpr int kRouteWaves = 4;
 constexpr float kSure = 0x1p-17f;
 
@@ -437,9 +437,9 @@ void plan_count_kernel(const PlanLaunch a)
 }
 
 // Bound by chains of loads: a wave holds the bins of its first 256 slots from the count to the sort, and all
-// threads share the counts of the runs.  Both launches, 160 thousand slots on 32 of 64 experts: 12.0 -> 7.8 us,
-// half of that by leaving out the slots of no expert here, whose one bin took half of the additions; 1.6
-// million slots on 64: 21.7 -> 16.7.
+// threads share the counts of the runs.  Both launches in a captured loop, 160 thousand slots on 32 of 64 experts:
+// 12.0 -> 7.7 us, half of that by leaving out the slots of no expert here, whose one bin took half of the
+// additions; 1.6 million slots on 64: 21.7 -> 16.2.
 __global__ __launch_bounds__(64 * kPlanWaves)
 void plan_kernel(const PlanLaunch a)
 {
@@ -672,9 +672,9 @@ hipError_t launch_route_experts(RouteLaunch a, int dtype, hipStream_t st)
     }
 }
 
-// One workgroup up to 4096 slots, above runs of 1024 (8192 slots: 6.6 us, 8.7 by one workgroup) and, where the
+// One workgroup up to 4096 slots, above runs of 1024 (8192 slots: 6.6 us, 9.1 by one workgroup) and, where the
 // counts of the runs before become the longer part, of 2048 for few experts (160 thousand slots, 32 experts:
-// 8.1 us, 9.1 with 4096) and of 4096 for many (512 experts: 12.9, 15.4 with 2048); at most 256 runs.
+// 7.7 us, 8.6 with 4096) and of 4096 for many (512 experts: 12.8, 15.1 with 2048); at most 256 runs.
 void plan_runs(int64_t S, int64_t E, int64_t &runs, int64_t &run)
 {
     constexpr int64_t step = 64 * kPlanWaves;

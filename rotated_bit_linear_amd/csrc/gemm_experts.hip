@@ -64,9 +64,9 @@ struct Stream {
     int8_t *pool;
 };
 
-// Products of up to 16 RM rows over rings of DW steps of weights and DA of the activation.  Weights that nobody else reads go past the caches (64
-// tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an expert has several blocks its weights
-// come from the cache the next time (777 tokens on 60: 31 us, not 36).
+// Products of up to 16 RM rows over rings of DW steps of weights and DA of the activation.  Weights that nobody
+// else reads go past the caches (64 tokens on 64 experts, 3584 x 5376: 106 -> 95 us, 6.5 TB/s); where an expert
+// has several blocks its weights come from the cache the next time (777 tokens on 60: 31 us, not 36).
 template <int OUT, bool SWIGLU, int RM, int DW, int DA>
 __device__ __forceinline__ void stream(const Stream &x)
 {
@@ -322,8 +322,10 @@ hipError_t launch_stream(const ExpertsGemm &g, hipStream_t st)
 }
 
 // Many rows an expert on average: 128-row tiles, whose waves share the weights in LDS.  64 experts, bf16, us
-// for 3584 x 5376 and 5376 x 1792, by streams and by tiles: 72 rows an expert 180 and 111, 204 and 111; 100
-// rows 221 and 141, 222 and 127.
+// for 3584 x 5376 and 5376 x 1792, by streams and by tiles: 72 rows an expert 171 and 107, 207 and 111; 88 rows
+// 197 and 122, 210 and 113; 100 rows 214 and 133, 218 and 118.  The average is over the experts here and counts
+// every slot, also those of experts elsewhere: how many fall here only the device knows (8 of 64 experts here, 128
+// tokens of 8 choices: 45 us by tiles, 16 by streams).
 bool tiled(int64_t S, int64_t E) { return S > 88 * E; }
 
 }  // namespace

@@ -2,7 +2,7 @@
 //
 // A workgroup takes one choice and 128 weight rows, 32 a wave.  It rotates and quantizes the choice's row
 // between the products for itself, while the first weights are on their way from memory: a launch less (one
-// token, 8 of 64 experts, 5376 and 1792 wide: 35.4 -> 32.1 us).  The codes then lie in LDS, so a wave only
+// token, 8 of 64 experts, 5376 and 1792 wide: 35.4 -> 32.5 us).  The codes then lie in LDS, so a wave only
 // waits for its own weights: no barrier a step.  Bound by HBM and by the launch.
 // Products as in gemm_experts.hip: 16 x 16 x 64 with the weights first; all 16 columns are the one row.
 // (The first product in this form, its row copied to LDS, takes 2.5 us more than with both operands in the
